@@ -70,7 +70,10 @@ typedef enum {
 /* Codes written to *err_word by the device. */
 #define VKV_DEVERR_TIMEOUT 1      /* a pipeline wait ran past its limit; outputs incomplete */
 #define VKV_DEVERR_BAD_INDEX 2    /* a block index lies outside the cache or the window     */
-#define VKV_DEVERR_BAD_OFFSETS 3  /* cu_seqlens decreasing or past the flattened cache      */
+#define VKV_DEVERR_BAD_OFFSETS 3  /* cu_seqlens decreasing or past the flattened cache; paged
+                                     cache: a length or ring position outside its range   */
+#define VKV_DEVERR_NO_SPACE 4     /* paged cache: not enough free pages, table columns or
+                                     token slots for the step; nothing was taken          */
 
 typedef enum {
   VKV_MODE_SEGMENTS = 0,
@@ -496,6 +499,183 @@ typedef struct {
 
 vkv_status vkv_latent_attn(const vkv_latent_args* args, vkv_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * Paged cache: single-token attention for a batch of rollouts ("rows") whose keys and
+ * values live in pages of `page` tokens, [n_pages, page, Hkv, d], named by a block table.
+ * Token t of row r is token t % page of page table[r][t / page].  A step is
+ *   vkv_page_map     new tokens -> pages and slots (device lengths, no host round trip)
+ *   vkv_page_append  their keys and values into the pages (and the pages' key means)
+ *   vkv_page_select  (optional) the pages each row and key head attends to
+ *   vkv_page_attn    one query per row over the row's cache
+ * Every count that changes from step to step (lengths, pages, tokens) is read on the
+ * device, so that a captured step can be replayed.  A length of -1 marks a row without
+ * a request everywhere.  Element offsets are 64-bit.  The segmented cache's mode-1 sets
+ * (sink frames + local window) and Sparse Forcing's coarse block selection (section 2
+ * components 2 and 3) keep their meaning, one query at a time.
+ * ---------------------------------------------------------------------------------- */
+typedef enum {
+  VKV_BF16 = 0,
+  VKV_FP16 = 1,
+  VKV_E4M3 = 2 /* 8-bit floating point (4 exponent, 3 mantissa bits, largest 448), cache only */
+} vkv_dtype;
+
+#define VKV_PAGE_MAX_ROWS 4096 /* rows of one call */
+
+/*
+ * vkv_page_map -- block table and slot map of one step, from the rows' lengths.
+ *
+ * Row r holds max(kv_len[r], 0) tokens and receives new_len[r] >= 0 more (a row with
+ * kv_len = -1 and new_len > 0 starts; with new_len = 0 it stays free); new_len = -1 ends
+ * the row's request: its pages go back and its length becomes -1.  Free pages are kept in
+ * a ring: entries ring[t % n_ring] for ring_pos[0] <= t < ring_pos[1].  Pages are taken
+ * from the front, in row order and within a row in token order, and written to the table;
+ * the pages of ended rows are returned behind the end, in row order and table order (they
+ * can be taken from the next call on).  New tokens are numbered in row order, cu[r] of
+ * them before row r; for token i of row r at position p:
+ *   row[i] = r, pos[i] = p, slot[i] = table[r][p / page] * page + p % page,
+ * and -1 in all three for i in [cu[R], max_tokens).
+ * A step that cannot be served whole changes nothing: kv_len_out = kv_len, ring_pos_out =
+ * ring_pos, cu = 0, slot = row = pos = -1, table and ring untouched, and the error word is
+ * VKV_DEVERR_NO_SPACE (too few free pages, or more tokens than max_tokens or than
+ * W * page in a row) or VKV_DEVERR_BAD_OFFSETS (a length below -1 or above W * page, ring
+ * positions that do not describe 0..n_ring free pages, or pages returned beyond n_ring).
+ * kv_len_out may be kv_len and ring_pos_out may be ring_pos.
+ */
+typedef struct {
+  int32_t R;               /* rows, 1..VKV_PAGE_MAX_ROWS                              */
+  int32_t W;               /* table columns, >= 1; R * W < 2^31                       */
+  int32_t page;            /* tokens per page, >= 1; W * page < 2^31                  */
+  int32_t n_ring;          /* capacity of the ring (the pool's pages), >= 1           */
+  int32_t max_tokens;      /* entries of slot, row and pos, >= 1                      */
+  int32_t reserved;        /* 0                                                       */
+  const int32_t* kv_len;   /* DEVICE [R]                                              */
+  const int32_t* new_len;  /* DEVICE [R]                                              */
+  int32_t* table;          /* DEVICE [R][W], row stride table_stride, updated in place */
+  int64_t table_stride;    /* elements, >= W                                          */
+  int32_t* ring;           /* DEVICE [n_ring], updated in place                       */
+  const int64_t* ring_pos; /* DEVICE [2]: pages taken, pages returned, since the start */
+  int32_t* kv_len_out;     /* DEVICE [R]: tokens held after the step                  */
+  int64_t* ring_pos_out;   /* DEVICE [2]                                              */
+  int64_t* slot;           /* DEVICE [max_tokens]                                     */
+  int32_t* row;            /* optional DEVICE [max_tokens]                            */
+  int32_t* pos;            /* optional DEVICE [max_tokens]                            */
+  int32_t* cu;             /* optional DEVICE [R + 1]                                 */
+  int32_t* err_word;       /* optional DEVICE int32                                   */
+} vkv_page_map_args;
+vkv_status vkv_page_map(const vkv_page_map_args* args, vkv_stream_t stream);
+
+/*
+ * vkv_page_append -- keys and values of a step's tokens into their slots.
+ *
+ * stored = x, or for a VKV_E4M3 cache e4m3(x / scale[head]) (fp32 quotient, round to
+ * nearest even, magnitudes above 448 become 448, NaN stays NaN).  Tokens with slot < 0 are
+ * skipped; a slot >= n_pages * page raises VKV_DEVERR_BAD_INDEX and is skipped.  Slots of
+ * one call are distinct (else it is open which token's row is kept).
+ * kbar (optional): receives, for each page written to, the mean of its stored keys
+ * (times k_scale) from the page's first token to the call's last one there, as fp32 -- the
+ * page's representative for vkv_page_select.  The call's tokens of one page then have to
+ * be consecutive, at consecutive slots, as vkv_page_map numbers them; the page's earlier
+ * rows are read from the cache, so a page that is written again from some token on gets
+ * the mean of what it then holds up to there.
+ */
+typedef struct {
+  int32_t T, Hkv, d;       /* tokens >= 0; key heads; d in {64, 128}                  */
+  int32_t page, n_pages;   /* tokens per page; pages of the cache                     */
+  int32_t x_dtype;         /* VKV_BF16 or VKV_FP16: k_new, v_new                      */
+  int32_t kv_dtype;        /* x_dtype or VKV_E4M3: the cache                          */
+  int32_t reserved;        /* 0                                                       */
+  vkv_tensor k_new, v_new; /* [T, Hkv, d]: st (token) and sh (head) strides, sb ignored */
+  vkv_tensor k, v;         /* cache [n_pages, page, Hkv, d]: sb page, st token, sh head */
+  const int64_t* slot;     /* DEVICE [T]                                              */
+  const float* k_scale;    /* DEVICE [Hkv], VKV_E4M3 only (NULL = 1)                  */
+  const float* v_scale;
+  float* kbar;             /* optional DEVICE [n_pages][Hkv][d], 16-byte aligned      */
+  int32_t* err_word;       /* optional DEVICE int32                                   */
+} vkv_page_append_args;
+vkv_status vkv_page_append(const vkv_page_append_args* args, vkv_stream_t stream);
+
+/*
+ * vkv_page_select -- the pages that one query per row attends to.
+ *
+ * Row r has n = ceil(kv_len[r] / page) pages.  For each key head g, kept are: the first
+ * sink_pages and the last local_pages, then the pages j with the highest coarse score
+ *   score(g, j) = < sum of the queries of the heads that share key head g, kbar[table[r][j]][g] >
+ * (fp64; a positive factor does not change the ranking; equal scores keep the lower j
+ * first; NaN ranks last), min(topk, n) pages in all.  sel receives their logical numbers
+ * j in ascending order, then -1.  A table entry outside [0, n_pages) raises
+ * VKV_DEVERR_BAD_INDEX and ranks last; a length below -1 or above W * page raises
+ * VKV_DEVERR_BAD_OFFSETS and counts as 0.  Rows of length 0 or -1 get -1 throughout.
+ */
+typedef struct {
+  int32_t R, H, Hkv, d;    /* rows; query heads (a multiple of Hkv); key heads; 64 or 128 */
+  int32_t page, n_pages;
+  int32_t W;               /* table columns; R * W < 2^31, W * page < 2^31            */
+  int32_t topk;            /* 1..4096, >= sink_pages + local_pages                    */
+  int32_t sink_pages, local_pages;
+  int32_t q_dtype;         /* VKV_BF16 or VKV_FP16                                    */
+  int32_t reserved;        /* 0                                                       */
+  vkv_tensor q;            /* [R, H, d]: sb row, sh head, st ignored                  */
+  const float* kbar;       /* DEVICE [n_pages][Hkv][d], 16-byte aligned               */
+  const int32_t* table;    /* DEVICE [R][W]                                           */
+  int64_t table_stride;
+  const int32_t* kv_len;   /* DEVICE [R]                                              */
+  int32_t* sel;            /* DEVICE [R][Hkv][topk]                                   */
+  void* workspace;         /* DEVICE, >= vkv_page_select_workspace_size(), 256-byte aligned */
+  size_t workspace_bytes;
+  int32_t* err_word;       /* optional DEVICE int32                                   */
+} vkv_page_select_args;
+size_t vkv_page_select_workspace_size(int32_t R, int32_t Hkv, int32_t W);
+vkv_status vkv_page_select(const vkv_page_select_args* args, vkv_stream_t stream);
+
+/*
+ * vkv_page_attn -- attention of one query per row over the row's paged cache.
+ *
+ * Query head h of row r reads key head h / (H / Hkv).  The visible tokens J are t <
+ * kv_len[r], and, when window > 0, of these only t < sink or t >= kv_len[r] - window
+ * (sink tokens + local window); when sel is given, only those of the selected pages.
+ *   s_t = scale * <q, k_t>,  o = sum_t softmax(s)_t v_t,  lse = ln sum_t exp(s_t),
+ * with k_t = k_scale[head] * stored for a VKV_E4M3 cache, values alike.  What the pages hold
+ * beyond the visible tokens (any bits) has no effect.  A row with no visible token gives
+ * o = 0 and lse = -inf; the outputs of a row with kv_len = -1 are left as they were.  A
+ * length below -1 or above W * page raises VKV_DEVERR_BAD_OFFSETS and its row's outputs
+ * are left as they were; a page number outside [0, n_pages) or a selected page outside
+ * [-1, W) raises VKV_DEVERR_BAD_INDEX and its tokens do not count (selected pages past the
+ * row's length do not count either).
+ * Long rows are split over the key axis and the parts joined by their LSEs, in an order
+ * that depends only on the sizes: equal inputs give equal bits.
+ * workspace: the first vkv_page_attn_workspace_size() bytes hold the parts and, at the
+ * front, counters that have to be zero before the first use and are zero again after each
+ * call (clear the buffer once); calls that may overlap on the GPU must not share one.
+ */
+typedef struct {
+  int32_t R, H, Hkv, d;    /* rows; query heads (a multiple of Hkv); key heads; 64 or 128 */
+  int32_t page, n_pages;
+  int32_t W;               /* table columns; R * W < 2^31, W * page < 2^31            */
+  int32_t q_dtype;         /* VKV_BF16 or VKV_FP16: q and o                           */
+  int32_t kv_dtype;        /* q_dtype or VKV_E4M3                                     */
+  float scale;             /* > 0                                                     */
+  int32_t sink, window;    /* tokens; window 0 = every token (sink is then ignored)   */
+  int32_t topk;            /* entries of a row of sel (0 when sel is NULL)            */
+  int32_t reserved;        /* 0                                                       */
+  vkv_tensor q, o;         /* [R, H, d]: sb row, sh head, st ignored                  */
+  vkv_tensor k, v;         /* [n_pages, page, Hkv, d]: sb page, st token, sh head     */
+  const int32_t* table;    /* DEVICE [R][W]                                           */
+  int64_t table_stride;
+  const int32_t* kv_len;   /* DEVICE [R]                                              */
+  const int32_t* sel;      /* optional DEVICE [R][Hkv][topk]: distinct logical pages, -1 = none;
+                              needs window = 0                                        */
+  const float* k_scale;    /* DEVICE [Hkv], VKV_E4M3 only (NULL = 1)                  */
+  const float* v_scale;
+  float* lse;              /* DEVICE [R][H]                                           */
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* err_word;       /* optional DEVICE int32                                   */
+} vkv_page_attn_args;
+/* Depends on H / Hkv, d and the number of SMs of the current device only; 0 for sizes
+ * that vkv_page_attn would refuse or without a usable device. */
+size_t vkv_page_attn_workspace_size(int32_t H, int32_t Hkv, int32_t d);
+vkv_status vkv_page_attn(const vkv_page_attn_args* args, vkv_stream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* vkv_status_string(vkv_status s);
 
@@ -505,7 +685,8 @@ int32_t vkv_version(void);
 /* sizeof() of the ABI structs, for bindings to check their layout:
  * 0 vkv_attn_args, 1 vkv_select_args, 2 vkv_tensor, 3 vkv_segment,
  * 4 vkv_compact_args, 5 vkv_head_rule, 6 vkv_persist_args, 7 vkv_latent_args,
- * 8 vkv_schedule; -1 otherwise. */
+ * 8 vkv_schedule, 9 vkv_page_map_args, 10 vkv_page_append_args,
+ * 11 vkv_page_select_args, 12 vkv_page_attn_args; -1 otherwise. */
 int32_t vkv_abi_sizeof(int32_t which);
 
 #ifdef __cplusplus

@@ -111,7 +111,7 @@ extern "C" const char* vkv_status_string(vkv_status s) {
   return "unknown status";
 }
 
-extern "C" int32_t vkv_version(void) { return 300; }
+extern "C" int32_t vkv_version(void) { return 400; }
 
 extern "C" int32_t vkv_abi_sizeof(int32_t which) {
   switch (which) {
@@ -124,6 +124,10 @@ extern "C" int32_t vkv_abi_sizeof(int32_t which) {
     case 6: return (int32_t)sizeof(vkv_persist_args);
     case 7: return (int32_t)sizeof(vkv_latent_args);
     case 8: return (int32_t)sizeof(vkv_schedule);
+    case 9: return (int32_t)sizeof(vkv_page_map_args);
+    case 10: return (int32_t)sizeof(vkv_page_append_args);
+    case 11: return (int32_t)sizeof(vkv_page_select_args);
+    case 12: return (int32_t)sizeof(vkv_page_attn_args);
   }
   return -1;
 }

@@ -1,0 +1,287 @@
+// vkv_page_map: pages and slots of one step's new tokens, from the rows' lengths.
+//
+// One thread-block cluster does the step.  Every CTA reads all rows (a few KB, from
+// L2 after the first) and scans them for itself: tokens, pages taken and pages returned
+// before each row.  So no CTA waits for another's result, and the tokens, the new table
+// entries and the returned pages can be spread over the cluster's threads, each of which
+// finds its row by bisection of the scan in shared memory.  The lengths and ring
+// positions may be updated in place: they are written only after a cluster barrier
+// behind every CTA's reads.
+//
+// Bound: latency.  A decoding step moves some tens of KB; its time is the launch, two
+// dependent reads (lengths, then ring or table) and the stores.
+#include <algorithm>
+#include <climits>
+#include <cstring>
+
+#include "vkv_internal.h"
+#include "vkv_ptx.cuh"
+
+namespace vkv {
+namespace {
+
+constexpr int kMapThreads = 512;
+constexpr int kMapMaxCluster = 8;
+
+struct MapParams {
+  int R, W, page, n_ring, max_tokens;
+  const int* kv_len;
+  const int* new_len;
+  int* table;
+  long long table_stride;
+  int* ring;
+  const long long* ring_pos;
+  int* kv_len_out;
+  long long* ring_pos_out;
+  long long* slot;
+  int* row;
+  int* pos;
+  int* cu;
+  int* err;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster; memory operations before it are visible after it.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Largest i in [0, n) with cu[i] <= x (cu ascending, cu[0] <= x).
+__device__ __forceinline__ int find_row(const int* cu, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Entry `i` (< n) behind position `first` (< n) of a ring of n < 2^31 entries.
+__device__ __forceinline__ unsigned ring_at(int first, int i, int n) {
+  const unsigned x = (unsigned)first + (unsigned)i;
+  return x >= (unsigned)n ? x - (unsigned)n : x;
+}
+
+__global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p) {
+  extern __shared__ int sm[];
+  int* tok = sm;               // [R + 1] new tokens before row r
+  int* need = tok + p.R + 1;   // [R + 1] pages taken before row r
+  int* back = need + p.R + 1;  // [R + 1] pages returned before row r
+  int* held = back + p.R + 1;  // [R] tokens held (0 for a free row)
+  __shared__ long long warp_tok[kMapThreads / 32];
+  __shared__ unsigned long long warp_pg[kMapThreads / 32];
+  __shared__ int fault;  // bit 0: a length out of range, bit 1: a row that does not fit its table row
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int R = p.R, page = p.page;
+  if (tid == 0) fault = 0;
+  const long long taken = p.ring_pos[0], returned = p.ring_pos[1];
+  const long long row_cap = (long long)p.W * page;
+  __syncthreads();
+  // each thread: `per` consecutive rows; 64-bit token sum, pages as need | back << 32
+  const int per = (R + kMapThreads - 1) / kMapThreads;
+  const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+  long long my_tok = 0;
+  unsigned long long my_pg = 0;
+  for (int r = r0; r < r1; ++r) {
+    int len = p.kv_len[r], add = p.new_len[r], bad = 0;
+    if (len < -1 || len > row_cap || add < -1) {
+      bad = 1;
+      len = add = 0;
+    } else if ((long long)max(len, 0) + max(add, 0) > row_cap) {
+      bad = 2;
+      add = 0;
+    }
+    if (bad) atomicOr(&fault, bad);
+    const int h = max(len, 0);
+    const unsigned had = (unsigned)(((long long)h + page - 1) / page);
+    unsigned nd = 0, bk = 0;
+    if (add < 0) bk = had;
+    else nd = (unsigned)(((long long)h + add + page - 1) / page) - had;
+    held[r] = h;
+    tok[r] = max(add, 0);
+    need[r] = (int)nd;
+    back[r] = (int)bk;
+    my_tok += max(add, 0);
+    my_pg += nd | ((unsigned long long)bk << 32);
+  }
+  long long it = my_tok;
+  unsigned long long ip = my_pg;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xFFFFFFFFu, it, o);
+    const unsigned long long b = __shfl_up_sync(0xFFFFFFFFu, ip, o);
+    if (lane >= o) {
+      it += a;
+      ip += b;
+    }
+  }
+  if (lane == 31) {
+    warp_tok[warp] = it;
+    warp_pg[warp] = ip;
+  }
+  __syncthreads();
+  long long base_t = it - my_tok, all_t = 0;
+  unsigned long long base_p = ip - my_pg, all_p = 0;
+#pragma unroll
+  for (int w = 0; w < kMapThreads / 32; ++w) {
+    if (w < warp) {
+      base_t += warp_tok[w];
+      base_p += warp_pg[w];
+    }
+    all_t += warp_tok[w];
+    all_p += warp_pg[w];
+  }
+  const unsigned n_need = (unsigned)all_p, n_back = (unsigned)(all_p >> 32);
+  // the step as a whole (the same decision in every thread of every CTA)
+  int bad = (fault & 1) ? VKV_DEVERR_BAD_OFFSETS : fault ? VKV_DEVERR_NO_SPACE : 0;
+  if (taken < 0 || returned < taken || returned - taken > p.n_ring ||
+      (long long)n_back > p.n_ring - (returned - taken))
+    bad = VKV_DEVERR_BAD_OFFSETS;
+  else if (!bad && (all_t > p.max_tokens || (long long)n_need > returned - taken))
+    bad = VKV_DEVERR_NO_SPACE;
+  if (!bad) {  // counts to offsets; sums fit (all_t <= max_tokens, pages <= n_ring)
+    int t = (int)base_t, a = (int)(unsigned)base_p, b = (int)(unsigned)(base_p >> 32);
+    for (int r = r0; r < r1; ++r) {
+      const int ct = tok[r], ca = need[r], cb = back[r];
+      tok[r] = t;
+      need[r] = a;
+      back[r] = b;
+      t += ct;
+      a += ca;
+      b += cb;
+    }
+    if (tid == 0) {
+      tok[R] = (int)all_t;
+      need[R] = (int)n_need;
+      back[R] = (int)n_back;
+    }
+  }
+  cluster_barrier();  // every CTA has read the lengths and positions; the scan is in shared memory
+  const int rank = (int)cluster_rank();
+  const int n_thr = (int)cluster_size() * kMapThreads, me = rank * kMapThreads + tid;
+  const int total = bad ? 0 : (int)all_t;
+  if (me == 0) {
+    if (bad && p.err) atomicCAS(p.err, 0, bad);
+    p.ring_pos_out[0] = bad ? taken : taken + n_need;
+    p.ring_pos_out[1] = bad ? returned : returned + n_back;
+  }
+  // a refused step's kv_len_out = kv_len: the lengths were not kept, and where the two are
+  // one array there is nothing to do
+  if (bad) {
+    if (p.kv_len_out != p.kv_len)
+      for (int r = me; r < R; r += n_thr) p.kv_len_out[r] = p.kv_len[r];
+  } else {
+    for (int r = me; r < R; r += n_thr) {
+      const int add = tok[r + 1] - tok[r];
+      // a row ends with new_len = -1; a free row that receives nothing stays free
+      const bool gone = p.new_len[r] < 0 || (add == 0 && p.kv_len[r] < 0);
+      p.kv_len_out[r] = gone ? -1 : held[r] + add;
+    }
+  }
+  if (p.cu)
+    for (int r = me; r <= R; r += n_thr) p.cu[r] = bad ? 0 : tok[r];
+  const int ring_t = (int)(taken % p.n_ring);
+  if (!bad) {
+    for (int i = me; i < (int)n_need; i += n_thr) {  // new table entries
+      const int r = find_row(need, R, i);
+      const int had = (int)(((long long)held[r] + page - 1) / page);
+      p.table[r * p.table_stride + had + (i - need[r])] = p.ring[ring_at(ring_t, i, p.n_ring)];
+    }
+    const int ring_b = (int)(returned % p.n_ring);
+    for (int i = me; i < (int)n_back; i += n_thr) {  // pages of ended rows
+      const int r = find_row(back, R, i);
+      p.ring[ring_at(ring_b, i, p.n_ring)] = p.table[r * p.table_stride + (i - back[r])];
+    }
+  }
+  for (int i = me; i < p.max_tokens; i += n_thr) {
+    long long s = -1;
+    int r = -1, t = -1;
+    if (i < total) {
+      r = find_row(tok, R, i);
+      t = held[r] + (i - tok[r]);
+      const int j = t / page, had = (int)(((long long)held[r] + page - 1) / page);
+      int pg;
+      if (j < had) {
+        pg = p.table[r * p.table_stride + j];
+      } else {
+        pg = p.ring[ring_at(ring_t, need[r] + (j - had), p.n_ring)];
+      }
+      s = (long long)pg * page + (t - j * page);
+      if (s < 0) s = -1;
+    }
+    p.slot[i] = s;
+    if (p.row) p.row[i] = r;
+    if (p.pos) p.pos[i] = t;
+  }
+}
+
+}  // namespace
+}  // namespace vkv
+
+using namespace vkv;
+
+extern "C" vkv_status vkv_page_map(const vkv_page_map_args* a, vkv_stream_t stream) {
+  if (!a) return VKV_ERR_NULL;
+  if (a->R < 1 || a->R > VKV_PAGE_MAX_ROWS || a->W < 1 || a->page < 1 || a->n_ring < 1 || a->max_tokens < 1)
+    return VKV_ERR_SHAPE;
+  if ((long long)a->R * a->W > INT_MAX || (long long)a->W * a->page > INT_MAX) return VKV_ERR_UNSUPPORTED;
+  if (a->table_stride < a->W) return VKV_ERR_SHAPE;
+  if (!a->kv_len || !a->new_len || !a->table || !a->ring || !a->ring_pos || !a->kv_len_out || !a->ring_pos_out ||
+      !a->slot)
+    return VKV_ERR_NULL;
+  int dev = 0;
+  if (device_sm_count(&dev) <= 0) return VKV_ERR_CUDA;
+  MapParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.R = a->R;
+  p.W = a->W;
+  p.page = a->page;
+  p.n_ring = a->n_ring;
+  p.max_tokens = a->max_tokens;
+  p.kv_len = a->kv_len;
+  p.new_len = a->new_len;
+  p.table = a->table;
+  p.table_stride = a->table_stride;
+  p.ring = a->ring;
+  p.ring_pos = reinterpret_cast<const long long*>(a->ring_pos);
+  p.kv_len_out = a->kv_len_out;
+  p.ring_pos_out = reinterpret_cast<long long*>(a->ring_pos_out);
+  p.slot = reinterpret_cast<long long*>(a->slot);
+  p.row = a->row;
+  p.pos = a->pos;
+  p.cu = a->cu;
+  p.err = a->err_word;
+  const int ctas = (int)std::min<long long>(kMapMaxCluster, ((long long)std::max(a->max_tokens, a->R) + kMapThreads - 1) / kMapThreads);
+  const size_t smem = (size_t)(4 * a->R + 3) * sizeof(int);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return VKV_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kMapThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)ctas;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, page_map_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return VKV_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? VKV_OK : VKV_ERR_CUDA;
+}

@@ -7,16 +7,19 @@ sm_100 device is present the calls raise.
 
 Raw entry points with the C names: ``vkv_chunk_attn``, ``vkv_block_select``,
 ``vkv_block_select_workspace_size``, ``vkv_lse_merge``, ``vkv_latent_attn``,
+``vkv_page_map``, ``vkv_page_append``, ``vkv_page_select``, ``vkv_page_attn``,
 ``vkv_status_string`` (and the other entry points of the header).
 Convenience wrappers that allocate outputs with torch: ``chunk_attn_segments``,
 ``chunk_attn_block_sparse``, ``chunk_attn_ragged``, ``block_select``, ``lse_merge``,
-``latent_attn`` and the others below.
+``latent_attn``, the paged cache's ``page_map``, ``page_append``, ``page_select`` and
+``page_attn``, and the others below.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import numpy as np
@@ -27,7 +30,8 @@ LIB_TEST_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvkv
 
 MODE_SEGMENTS, MODE_BLOCK_SPARSE, MODE_RAGGED = 0, 1, 2
 MAX_BRANCHES, MAX_SEGMENTS = 2, 8
-DEVERR_TIMEOUT, DEVERR_BAD_INDEX, DEVERR_BAD_OFFSETS = 1, 2, 3
+DEVERR_TIMEOUT, DEVERR_BAD_INDEX, DEVERR_BAD_OFFSETS, DEVERR_NO_SPACE = 1, 2, 3, 4
+DTYPE_BF16, DTYPE_FP16, DTYPE_E4M3 = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 4 * 1024 * 1024  # VKV_NOALLOC_SCRATCH_BYTES in include/vkv.h
 STATUS = {0: "VKV_OK", 1: "VKV_ERR_NULL", 2: "VKV_ERR_SHAPE", 3: "VKV_ERR_ALIGN", 4: "VKV_ERR_RANGE",
           5: "VKV_ERR_UNSUPPORTED", 6: "VKV_ERR_CUDA", 7: "VKV_ERR_WORKSPACE"}
@@ -120,6 +124,49 @@ class vkv_latent_args(ctypes.Structure):
         ("lse", c_void_p), ("err_word", c_void_p),
     ]
 
+class vkv_page_map_args(ctypes.Structure):
+    _fields_ = [
+        ("R", c_int32), ("W", c_int32), ("page", c_int32), ("n_ring", c_int32), ("max_tokens", c_int32),
+        ("reserved", c_int32),
+        ("kv_len", c_void_p), ("new_len", c_void_p), ("table", c_void_p), ("table_stride", c_int64),
+        ("ring", c_void_p), ("ring_pos", c_void_p), ("kv_len_out", c_void_p), ("ring_pos_out", c_void_p),
+        ("slot", c_void_p), ("row", c_void_p), ("pos", c_void_p), ("cu", c_void_p), ("err_word", c_void_p),
+    ]
+
+
+class vkv_page_append_args(ctypes.Structure):
+    _fields_ = [
+        ("T", c_int32), ("Hkv", c_int32), ("d", c_int32), ("page", c_int32), ("n_pages", c_int32),
+        ("x_dtype", c_int32), ("kv_dtype", c_int32), ("reserved", c_int32),
+        ("k_new", vkv_tensor), ("v_new", vkv_tensor), ("k", vkv_tensor), ("v", vkv_tensor),
+        ("slot", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p), ("kbar", c_void_p),
+        ("err_word", c_void_p),
+    ]
+
+
+class vkv_page_select_args(ctypes.Structure):
+    _fields_ = [
+        ("R", c_int32), ("H", c_int32), ("Hkv", c_int32), ("d", c_int32), ("page", c_int32), ("n_pages", c_int32),
+        ("W", c_int32), ("topk", c_int32), ("sink_pages", c_int32), ("local_pages", c_int32),
+        ("q_dtype", c_int32), ("reserved", c_int32),
+        ("q", vkv_tensor), ("kbar", c_void_p), ("table", c_void_p), ("table_stride", c_int64),
+        ("kv_len", c_void_p), ("sel", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+        ("err_word", c_void_p),
+    ]
+
+
+class vkv_page_attn_args(ctypes.Structure):
+    _fields_ = [
+        ("R", c_int32), ("H", c_int32), ("Hkv", c_int32), ("d", c_int32), ("page", c_int32), ("n_pages", c_int32),
+        ("W", c_int32), ("q_dtype", c_int32), ("kv_dtype", c_int32), ("scale", c_float), ("sink", c_int32),
+        ("window", c_int32), ("topk", c_int32), ("reserved", c_int32),
+        ("q", vkv_tensor), ("o", vkv_tensor), ("k", vkv_tensor), ("v", vkv_tensor),
+        ("table", c_void_p), ("table_stride", c_int64), ("kv_len", c_void_p), ("sel", c_void_p),
+        ("k_scale", c_void_p), ("v_scale", c_void_p), ("lse", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("err_word", c_void_p),
+    ]
+
+
 class vkv_schedule(ctypes.Structure):
     _fields_ = [
         ("n_ctas", c_int32), ("n_units", c_int32), ("n_pieces", c_int32), ("n_slots", c_int32),
@@ -207,8 +254,17 @@ def _load(path: str) -> ctypes.CDLL:
     L.vkv_persist_update.restype = c_int32
     L.vkv_latent_attn.argtypes = [POINTER(vkv_latent_args), c_void_p]
     L.vkv_latent_attn.restype = c_int32
+    for name in ("vkv_page_map", "vkv_page_append", "vkv_page_select", "vkv_page_attn"):
+        fn = getattr(L, name)
+        fn.argtypes = [c_void_p, c_void_p]  # a struct by reference, or its packed bytes
+        fn.restype = c_int32
+    L.vkv_page_select_workspace_size.argtypes = [c_int32] * 3
+    L.vkv_page_select_workspace_size.restype = c_size_t
+    L.vkv_page_attn_workspace_size.argtypes = [c_int32] * 3
+    L.vkv_page_attn_workspace_size.restype = c_size_t
     for i, st in enumerate((vkv_attn_args, vkv_select_args, vkv_tensor, vkv_segment, vkv_compact_args,
-                            vkv_head_rule, vkv_persist_args, vkv_latent_args, vkv_schedule)):
+                            vkv_head_rule, vkv_persist_args, vkv_latent_args, vkv_schedule,
+                            vkv_page_map_args, vkv_page_append_args, vkv_page_select_args, vkv_page_attn_args)):
         if L.vkv_abi_sizeof(i) != ctypes.sizeof(st):
             raise RuntimeError(f"ABI mismatch for {st.__name__}: C {L.vkv_abi_sizeof(i)} B, "
                                f"binding {ctypes.sizeof(st)} B")
@@ -289,6 +345,30 @@ def vkv_persist_update(args: vkv_persist_args, stream: int | None) -> int:
 
 def vkv_latent_attn(args: vkv_latent_args, stream: int | None) -> int:
     return int(lib().vkv_latent_attn(ctypes.byref(args), c_void_p(stream or 0)))
+
+
+def vkv_page_map(args: vkv_page_map_args, stream: int | None) -> int:
+    return int(lib().vkv_page_map(ctypes.byref(args), c_void_p(stream or 0)))
+
+
+def vkv_page_append(args: vkv_page_append_args, stream: int | None) -> int:
+    return int(lib().vkv_page_append(ctypes.byref(args), c_void_p(stream or 0)))
+
+
+def vkv_page_select(args: vkv_page_select_args, stream: int | None) -> int:
+    return int(lib().vkv_page_select(ctypes.byref(args), c_void_p(stream or 0)))
+
+
+def vkv_page_attn(args: vkv_page_attn_args, stream: int | None) -> int:
+    return int(lib().vkv_page_attn(ctypes.byref(args), c_void_p(stream or 0)))
+
+
+def vkv_page_select_workspace_size(R, Hkv, W) -> int:
+    return int(lib().vkv_page_select_workspace_size(R, Hkv, W))
+
+
+def vkv_page_attn_workspace_size(H, Hkv, d) -> int:
+    return int(lib().vkv_page_attn_workspace_size(H, Hkv, d))
 
 
 def vkv_debug_withhold_copy(n_calls: int) -> int:
@@ -664,3 +744,242 @@ def latent_attn(q, kv, d_c, scale=None, kr=None, err=None, stream=None, out=None
     a.err_word = err.data_ptr() if err is not None else None
     _check(vkv_latent_attn(a, _stream(stream)), "vkv_latent_attn")
     return o, l
+
+
+# ---------------------------------------------------------------------------
+# paged cache: one query per row (request) over pages of tokens
+# ---------------------------------------------------------------------------
+# These calls run once per layer and token, so their arguments are packed by struct
+# (the C layout, checked against the ctypes structures) instead of field by field.
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float8_e4m3fn: DTYPE_E4M3}
+_T = "Pqqq"  # a vkv_tensor
+_PAGE_MAP = struct.Struct("@6i3Pq9P")
+_PAGE_APPEND = struct.Struct("@8i" + 4 * _T + "5P")
+_PAGE_SELECT = struct.Struct("@12i" + _T + "PPqPPPNP")
+_PAGE_ATTN = struct.Struct("@9if4i" + 4 * _T + "PqPPPPPPNP")
+for _fmt, _cls in ((_PAGE_MAP, vkv_page_map_args), (_PAGE_APPEND, vkv_page_append_args),
+                   (_PAGE_SELECT, vkv_page_select_args), (_PAGE_ATTN, vkv_page_attn_args)):
+    if _fmt.size != ctypes.sizeof(_cls):
+        raise RuntimeError(f"packed layout of {_cls.__name__}: {_fmt.size} B, expected {ctypes.sizeof(_cls)} B")
+
+_page_attn_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, cleared once (the call leaves it clear)
+_page_select_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, grown on demand
+
+
+def _on(device, stream, *tensors):
+    """The stream handle for a call on `device`, after checking that every tensor lives there."""
+    for x in tensors:
+        if x is not None and x.device != device:
+            raise ValueError(f"tensors on different devices: {x.device} and {device}")
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _call_page(name, fmt, device, sh, *values):
+    """One C call under `device`; raises VkvError on a non-OK status."""
+    fn = getattr(_lib or lib(), name)
+    if device.index == torch._C._cuda_getDevice():
+        status = fn(fmt.pack(*values), sh)
+    else:
+        with torch.cuda.device(device):
+            status = fn(fmt.pack(*values), sh)
+    if status:
+        _check(status, name)
+
+
+def _ints(x, what, dtype, *shape):
+    """`x`, checked to be a contiguous `dtype` tensor of `shape` (None entries are free)."""
+    if x.dtype != dtype or not x.is_contiguous() or x.dim() != len(shape) or any(
+            want is not None and have != want for have, want in zip(x.shape, shape)):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape}, got {x.dtype} {tuple(x.shape)}")
+    return x
+
+
+def _ptr(x):
+    return 0 if x is None else x.data_ptr()
+
+
+def _page_table(table, R):
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != R or (
+            table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("block_table must be an int32 tensor [R, W] with contiguous rows")
+    # a single row's stride is never used; a narrower one than W means overlapping rows
+    return max(table.stride(0), table.shape[1]) if R == 1 else table.stride(0)
+
+
+def _cache(k, v):
+    """(pages, tokens per page, key heads, d, dtype code) of a paged cache pair."""
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride(3) != 1 or v.stride(3) != 1:
+        raise ValueError("k_pages and v_pages must be [n_pages, page, Hkv, d] of one type with contiguous d")
+    return (*k.shape, _dtype(k, "the cache"))
+
+
+def _dtype(x, what):
+    try:
+        return _DTYPES[x.dtype]
+    except KeyError:
+        raise ValueError(f"{what}: {x.dtype} is not one of bfloat16, float16, float8_e4m3fn") from None
+
+
+def _scales(k_scale, v_scale, kv_dtype, Hkv):
+    if k_scale is None and v_scale is None:
+        return
+    if kv_dtype != DTYPE_E4M3:
+        raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache")
+    for x, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if x is not None:
+            _ints(x, what, torch.float32, Hkv)
+
+
+def page_map(kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens, out=None, err=None, stream=None):
+    """Pages and slots of one step's new tokens (vkv_page_map).
+
+    kv_len, new_len: int32 [R] tokens held (-1: no request) and arriving (-1: the request
+    ends).  block_table int32 [R, W] and ring int32 [n] (free page numbers, ring[t % n] for
+    ring_pos[0] <= t < ring_pos[1]) are updated in place; ring_pos int64 [2].
+    Returns (or fills `out`) dict(kv_len, ring [the new ring_pos], slot int64 [max_tokens],
+    row, pos int32 [max_tokens], cu int32 [R + 1]); out["kv_len"] may be kv_len itself and
+    out["ring"] ring_pos.  A step that does not fit changes nothing and sets err.
+    """
+    R, dev = kv_len.shape[0], kv_len.device
+    max_tokens = int(max_tokens)
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=dev)
+        out = {"kv_len": torch.empty(R, **i32), "ring": torch.empty(2, dtype=torch.int64, device=dev),
+               "slot": torch.empty(max_tokens, dtype=torch.int64, device=dev),
+               "row": torch.empty(max_tokens, **i32), "pos": torch.empty(max_tokens, **i32),
+               "cu": torch.empty(R + 1, **i32)}
+    row, pos, cu = out.get("row"), out.get("pos"), out.get("cu")
+    sh = _on(dev, stream, new_len, block_table, ring, ring_pos, out["kv_len"], out["ring"], out["slot"], row, pos, cu,
+             err)
+    _ints(kv_len, "kv_len", torch.int32, R)
+    _ints(new_len, "new_len", torch.int32, R)
+    _ints(ring, "ring", torch.int32, None)
+    _ints(ring_pos, "ring_pos", torch.int64, 2)
+    _ints(out["kv_len"], "out['kv_len']", torch.int32, R)
+    _ints(out["ring"], "out['ring']", torch.int64, 2)
+    _ints(out["slot"], "out['slot']", torch.int64, max_tokens)
+    for x, what, n in ((row, "row", max_tokens), (pos, "pos", max_tokens), (cu, "cu", R + 1)):
+        if x is not None:
+            _ints(x, f"out['{what}']", torch.int32, n)
+    stride = _page_table(block_table, R)
+    _call_page("vkv_page_map", _PAGE_MAP, dev, sh, R, block_table.shape[1], int(page_size), ring.shape[0], max_tokens, 0,
+               kv_len.data_ptr(), new_len.data_ptr(), block_table.data_ptr(), stride, ring.data_ptr(),
+               ring_pos.data_ptr(), out["kv_len"].data_ptr(), out["ring"].data_ptr(), out["slot"].data_ptr(),
+               _ptr(row), _ptr(pos), _ptr(cu), _ptr(err))
+    return out
+
+
+def page_append(k_new, v_new, slot, k_pages, v_pages, k_scale=None, v_scale=None, kbar=None, err=None, stream=None):
+    """Write a step's keys and values [T, Hkv, d] into the pages at `slot` (vkv_page_append).
+
+    k_pages, v_pages [n_pages, page, Hkv, d] of the type of k_new, or float8_e4m3fn (stored =
+    x / scale, fp32 scales [Hkv]); kbar (optional fp32 [n_pages, Hkv, d]) receives the key
+    mean of each page written to.
+    """
+    N, P, Hkv, d, kv_dtype = _cache(k_pages, v_pages)
+    T, dev = k_new.shape[0], k_pages.device
+    if k_new.shape != (T, Hkv, d) or v_new.shape != k_new.shape or k_new.dtype != v_new.dtype or (
+            k_new.stride(2) != 1 or v_new.stride(2) != 1):
+        raise ValueError("k_new and v_new must be [T, Hkv, d] of one type with contiguous d")
+    sh = _on(dev, stream, v_pages, k_new, v_new, slot, k_scale, v_scale, kbar, err)
+    _ints(slot, "slot", torch.int64, T)
+    _scales(k_scale, v_scale, kv_dtype, Hkv)
+    if kbar is not None:
+        _ints(kbar, "kbar", torch.float32, N, Hkv, d)
+    _call_page("vkv_page_append", _PAGE_APPEND, dev, sh, T, Hkv, d, P, N, _dtype(k_new, "k_new"), kv_dtype, 0,
+               k_new.data_ptr(), 0, k_new.stride(0), k_new.stride(1),
+               v_new.data_ptr(), 0, v_new.stride(0), v_new.stride(1),
+               k_pages.data_ptr(), *k_pages.stride()[:3], v_pages.data_ptr(), *v_pages.stride()[:3],
+               slot.data_ptr(), _ptr(k_scale), _ptr(v_scale), _ptr(kbar), _ptr(err))
+
+
+def _page_workspace(kept, device, sh, need, clear):
+    """A workspace of `need` bytes for a call on (device, stream): one kept by this module,
+    or, while the stream is being captured, one of the graph's own (two captured graphs
+    may be replayed at the same time, so they must not share it)."""
+    if sh != torch._C._cuda_getCurrentRawStream(device.index) or device.index != torch._C._cuda_getDevice():
+        # allocate, clear and ask about a capture on the stream that will use it
+        on = torch.cuda.ExternalStream(sh, device=device) if sh else torch.cuda.default_stream(device)
+        with torch.cuda.stream(on):
+            return _page_workspace(kept, device, sh, need, clear)
+    if torch.cuda.is_current_stream_capturing():
+        return (torch.zeros if clear else torch.empty)(need, dtype=torch.uint8, device=device)
+    key = (device.index, sh)
+    buf = kept.get(key)
+    if buf is None or buf.numel() < need:
+        buf = (torch.zeros if clear else torch.empty)(need, dtype=torch.uint8, device=device)
+        kept[key] = buf
+    return buf
+
+
+def page_select(q, kbar, block_table, kv_len, page_size, topk, sink_pages=0, local_pages=0, err=None, stream=None,
+                out=None, workspace=None):
+    """The `topk` pages that each row and key head attends to (vkv_page_select).
+
+    q [R, H, d]; kbar fp32 [n_pages, Hkv, d], the pages' key means (page_append keeps them).
+    Returns int32 [R, Hkv, topk]: logical page numbers ascending, then -1.
+    """
+    R, H, d = q.shape
+    N, Hkv, dk = kbar.shape
+    dev = q.device
+    topk = int(topk)
+    if dk != d or q.stride(2) != 1:
+        raise ValueError("q must be [R, H, d] with contiguous d, kbar [n_pages, Hkv, d]")
+    sel = out if out is not None else torch.empty((R, Hkv, topk), dtype=torch.int32, device=dev)
+    sh = _on(dev, stream, kbar, block_table, kv_len, sel, workspace, err)
+    _ints(kbar, "kbar", torch.float32, N, Hkv, d)
+    _ints(kv_len, "kv_len", torch.int32, R)
+    _ints(sel, "out", torch.int32, R, Hkv, topk)
+    table_stride, W = _page_table(block_table, R), block_table.shape[1]
+    if workspace is None:
+        workspace = _page_workspace(_page_select_ws, dev, sh, vkv_page_select_workspace_size(R, Hkv, W), False)
+    _call_page("vkv_page_select", _PAGE_SELECT, dev, sh, R, H, Hkv, d, int(page_size), N, W, topk, int(sink_pages),
+               int(local_pages), _dtype(q, "q"), 0, q.data_ptr(), q.stride(0), 0, q.stride(1), kbar.data_ptr(),
+               block_table.data_ptr(), table_stride, kv_len.data_ptr(), sel.data_ptr(), workspace.data_ptr(),
+               workspace.numel() * workspace.element_size(), _ptr(err))
+    return sel
+
+
+def page_attn(q, k_pages, v_pages, block_table, kv_len, scale=None, sink=0, window=0, sel=None, k_scale=None,
+              v_scale=None, err=None, stream=None, out=None, workspace=None):
+    """Attention of one query per row over its paged cache (vkv_page_attn).
+
+    q [R, H, d] bf16 or fp16; k_pages, v_pages [n_pages, page, Hkv, d] of q's type or
+    float8_e4m3fn with fp32 scales [Hkv]; kv_len int32 [R] (-1: no request, its outputs are
+    left as they were).  window > 0 keeps the first `sink` and the last `window` tokens; sel
+    (from page_select) the selected pages.  Returns (o [R, H, d], lse fp32 [R, H]).
+    workspace: a uint8 tensor whose contents were zero before its first use.
+    """
+    R, H, d = q.shape
+    N, P, Hkv, dk, kv_dtype = _cache(k_pages, v_pages)
+    dev = q.device
+    if dk != d or q.stride(2) != 1:
+        raise ValueError("q must be [R, H, d] with contiguous d, the d of the cache")
+    if out is None:
+        o, lse = (torch.empty((R, H, d), dtype=q.dtype, device=dev), torch.empty((R, H), dtype=torch.float32, device=dev))
+    else:
+        o, lse = out
+    if o.shape != q.shape or o.dtype != q.dtype or o.stride(2) != 1:
+        raise ValueError("o must have the shape and type of q, with contiguous d")
+    sh = _on(dev, stream, k_pages, v_pages, block_table, kv_len, sel, k_scale, v_scale, o, lse, workspace, err)
+    _ints(kv_len, "kv_len", torch.int32, R)
+    _ints(lse, "lse", torch.float32, R, H)
+    _scales(k_scale, v_scale, kv_dtype, Hkv)
+    topk = 0
+    if sel is not None:
+        topk = sel.shape[-1]
+        _ints(sel, "sel", torch.int32, R, Hkv, topk)
+    table_stride = _page_table(block_table, R)
+    if workspace is None:
+        workspace = _page_workspace(_page_attn_ws, dev, sh, vkv_page_attn_workspace_size(H, Hkv, d), True)
+    _call_page("vkv_page_attn", _PAGE_ATTN, dev, sh, R, H, Hkv, d, P, N, block_table.shape[1], _dtype(q, "q"), kv_dtype,
+               float(scale if scale is not None else d ** -0.5), int(sink), int(window), topk, 0,
+               q.data_ptr(), q.stride(0), 0, q.stride(1), o.data_ptr(), o.stride(0), 0, o.stride(1),
+               k_pages.data_ptr(), *k_pages.stride()[:3], v_pages.data_ptr(), *v_pages.stride()[:3],
+               block_table.data_ptr(), table_stride, kv_len.data_ptr(), _ptr(sel), _ptr(k_scale), _ptr(v_scale),
+               lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(err))
+    return o, lse

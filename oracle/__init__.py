@@ -6,7 +6,8 @@ leg of ``bench.py`` may import it.  It shares no code with the library.
 
 Parity status: every function here is pinned by ``tests/test_oracle_pins.py``
 (brute force, closed forms, invariants and hand-worked cases in
-``tests/golden/``); none is unpinned.
+``tests/golden/``), the paged cache's by ``tests/test_oracle_paged.py``; none is
+unpinned.
 """
 from .attention import (  # noqa: F401
     attend,
@@ -28,3 +29,4 @@ from .attention import (  # noqa: F401
 from .compaction import compact_cache, head_frames, merge_frames  # noqa: F401
 from .memory import persist_update  # noqa: F401
 from .mla import latent_attention, visited_flops_latent  # noqa: F401
+from .paged import page_attn, page_map, page_means, page_select  # noqa: F401
