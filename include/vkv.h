@@ -662,8 +662,8 @@ typedef struct {
   const int32_t* table;    /* DEVICE [R][W]                                           */
   int64_t table_stride;
   const int32_t* kv_len;   /* DEVICE [R]                                              */
-  const int32_t* sel;      /* optional DEVICE [R][Hkv][topk]: distinct logical pages, -1 = none;
-                              needs window = 0                                        */
+  const int32_t* sel;      /* optional DEVICE [R][Hkv][topk]: distinct logical pages, of which the
+                              first min(topk, ceil(kv_len / page)) are read; -1 = none; needs window = 0 */
   const float* k_scale;    /* DEVICE [Hkv], VKV_E4M3 only (NULL = 1)                  */
   const float* v_scale;
   float* lse;              /* DEVICE [R][H]                                           */

@@ -1,19 +1,53 @@
 // vkv_page_attn: attention of one query per row over the row's paged cache.
 //
-// First form: one CTA per (row, query head).  Each of its warps takes every fourth
-// visible token, the lanes share the head dimension, and each warp keeps a running
-// maximum, sum and output; the warps' parts meet in shared memory.
+//   s_t = scale <q_h, k_t>,  o = sum_t 2^(c s_t - m) v_t / sum_t 2^(c s_t - m),  c = scale log2 e
+//
+// Every cached byte is used by the G = H / Hkv queries that share its head and by nothing
+// else: 4 G flops per 16-bit key-value pair of numbers, far below what the tensor cores
+// could do meanwhile, so HBM bounds the call and the kernel is built as a stream.
+//
+// Work: the visible tokens of a (row, key head, chunk of up to 16 query heads) are a unit,
+// cut into tiles of TT tokens; all units' tiles form one line, which is dealt out to the
+// warps of a grid of two blocks per SM in equal contiguous shares.  So rows of any length
+// mix, one long row fills the GPU, and no host code needs the lengths.  Each warp streams
+// its own share through a private ring of cp.async stages (K and V of a tile, addresses from
+// the block table, masked tokens zero-filled); warps never wait for one another until the
+// end.  A unit within one warp's share is finished there.  A unit cut by shares leaves its
+// parts (m, l, O) in shared memory, one block joins its own, and parts of a unit that spans
+// blocks go to the workspace, where the block that arrives last joins them, in block order:
+// no atomics on data, equal inputs give equal bits.
+//
+// Arithmetic: S^T = K Q^T and O^T = V^T P^T by m16n8k16 instructions: the many tokens (and
+// the d output channels) fill the 16-wide side, the few heads the 8-wide one.  16-bit
+// caches multiply in their own type; an 8-bit cache is widened to f16 (exact), with bf16
+// queries first scaled by a power of two of each head so that they fit f16: what that
+// drops is below 2^-38 of the head's largest query element.  The weights P go in as two
+// 16-bit parts (value and remainder), so that no rounding of P to 16 bits is left; sums and
+// outputs are fp32.  The running maximum only moves when a score exceeds it by 2^4.
 #include <algorithm>
 #include <climits>
 #include <cstring>
+#include <type_traits>
 
 #include "vkv_page.cuh"
 
 namespace vkv {
 namespace {
 
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kBlocksPerSm = 2;
+constexpr int kMaxBlocks = kBlocksPerSm * kMaxCtas;
+constexpr float kSlack = 4.f;  // log2: how far a score may exceed the running maximum
+#ifndef VKV_PAGE_MIN_TILES
+#define VKV_PAGE_MIN_TILES 2
+#endif
+constexpr int kMinTiles = VKV_PAGE_MIN_TILES;  // least share of a warp
+
 struct PageAttnParams {
   int R, H, Hkv, G, page, n_pages, W, sink, window, topk;
+  uint32_t div_mul, div_shift;  // n / page = (umulhi(n, mul) + n) >> shift, n < 2^31
+  int n_chunks;                 // chunks of query heads per key head
   float scale_log2;
   const void* q;
   long long q_sb, q_sh;
@@ -29,116 +63,729 @@ struct PageAttnParams {
   const float* ks;
   const float* vs;
   float* lse;
+  int* counters;  // [blocks]
+  float* ws_ml;   // [2 * blocks][heads of a chunk][2]: maximum, sum
+  float* ws_o;    // [2 * blocks][heads of a chunk][d]
   int* err;
 };
 
-template <typename T>
-__device__ __forceinline__ T from_float(float f);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float f) { return __float2bfloat16_rn(f); }
-template <>
-__device__ __forceinline__ __half from_float(float f) { return __float2half_rn(f); }
-
-template <typename T, bool E4M3>
-__device__ __forceinline__ float elem(const char* row, int c) {
-  if constexpr (E4M3) {
-    const uint32_t h2 = e4m3x2_to_f16x2(reinterpret_cast<const uint8_t*>(row)[c]);
-    return __low2float(*reinterpret_cast<const __half2*>(&h2));
+// ---------------------------------------------------------------------------------------
+// instructions
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const char* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// D (16x8, fp32) += A (16x16) B (16x8), 16-bit operands
+template <typename M>
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (std::is_same<M, __nv_bfloat16>::value) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   } else {
-    return (float)reinterpret_cast<const T*>(row)[c];
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
 }
-
-constexpr int kSimpleWarps = 4;
-
-template <int D, typename T, bool E4M3>
-__global__ void __launch_bounds__(kSimpleWarps * 32) page_attn_kernel(const PageAttnParams p) {
-  constexpr int PL = D / 32;
-  __shared__ float sm_m[kSimpleWarps], sm_l[kSimpleWarps], sm_o[kSimpleWarps][D];
-  const int r = blockIdx.x / p.H, h = blockIdx.x - r * p.H, g = h / p.G;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int len = page_row_len(p.kv_len[r], p.W, p.page, p.err);
-  if (len < 0) return;
-  const T* q = reinterpret_cast<const T*>(p.q) + r * p.q_sb + h * p.q_sh;
-  const float ks = (E4M3 && p.ks ? p.ks[g] : 1.f) * p.scale_log2, vs = E4M3 && p.vs ? p.vs[g] : 1.f;
-  float qr[PL], acc[PL], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    qr[i] = (float)q[lane + 32 * i];
-    acc[i] = 0.f;
+template <typename M>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (std::is_same<M, __nv_bfloat16>::value) {
+    return pack_bf16x2(lo, hi);
+  } else {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
   }
-  const int* sel = p.sel ? p.sel + ((long long)r * p.Hkv + g) * p.topk : nullptr;
-  const int lo = p.window > 0 ? min(p.sink, len) : len;
-  const int gap = p.window > 0 ? max(0, len - p.window - lo) : 0;
-  const long long count = p.sel ? (long long)p.topk * p.page : (long long)len - gap;
-  for (long long x = warp; x < count; x += kSimpleWarps) {
-    long long tok;
-    if (sel) {
-      const int j = sel[x / p.page];
-      if (j < 0 || j >= p.W) {
-        if (j != -1 && p.err && lane == 0) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
-        continue;
-      }
-      tok = (long long)j * p.page + x % p.page;
-      if (tok >= len) continue;
-    } else {
-      tok = x < lo ? x : x + gap;
+}
+template <typename M>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (std::is_same<M, __nv_bfloat16>::value)
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// ---------------------------------------------------------------------------------------
+// sizes of a variant
+// ---------------------------------------------------------------------------------------
+template <int D, bool F8, int NT>
+struct Shape {
+  static constexpr int RB = F8 ? D : 2 * D;        // bytes of a token's row of one head
+  static constexpr int CPR = RB / 16;              // 16-byte pieces of it
+  static constexpr int TT = RB == 256 ? 16 : 32;   // tokens per tile: 8 KB of K and V (4 KB for 64-byte rows)
+  static constexpr int MT = TT / 16;
+  static constexpr int S = NT == 1 ? 3 : 2;        // stages per warp (two blocks' shared memory fits an SM)
+  static constexpr int HC = 8 * NT;                // heads of a chunk
+  static constexpr int TILE = TT * RB;             // bytes of K (or V) in a stage
+  static constexpr int LD = D + 4;                 // floats between a part's heads (conflict-free accumulator
+                                                   // stores); D and D + 1 hold the head's maximum and sum
+  static constexpr int PART = HC * LD * 4;         // bytes of a part's O
+  static constexpr int WARP = S * 2 * TILE;        // bytes of a warp's ring; a last part is left in it
+  static constexpr int SMEM = kWarps * (WARP + PART);
+  static_assert(WARP >= PART, "a part fits the ring");
+};
+
+// Where a row's 16-byte piece lies in a tile: pieces of one column of 8 rows hit 8 bank groups.
+template <int RB>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+  if constexpr (RB >= 128)
+    return (uint32_t)(row * RB + ((piece ^ (row & 7)) << 4));
+  else
+    return (uint32_t)(row * RB + ((piece ^ ((row >> 1) & 3)) << 4));
+}
+
+struct Part {  // what a warp leaves of a cut unit; valid: te > tb
+  int r, u, tb, te, tiles;
+  long long unit0;  // the unit's first tile on the line
+};
+
+// Shares: the line's first `rem` shares have q + 1 tiles, the others q.
+struct Shares {
+  long long q, rem;
+  __device__ __forceinline__ long long begin(long long w) const { return w * q + min(w, rem); }
+  __device__ __forceinline__ int warp_of(long long x) const {
+    const long long cut = rem * (q + 1);
+    return (int)(x < cut ? x / (q + 1) : rem + (x - cut) / q);
+  }
+};
+
+template <int D>
+struct Vec;
+template <>
+struct Vec<128> { using type = float4; };
+template <>
+struct Vec<64> { using type = float2; };
+
+__device__ __forceinline__ void axpy(float4& a, float w, const float4 x) {
+  a.x = fmaf(w, x.x, a.x); a.y = fmaf(w, x.y, a.y); a.z = fmaf(w, x.z, a.z); a.w = fmaf(w, x.w, a.w);
+}
+__device__ __forceinline__ void axpy(float2& a, float w, const float2 x) {
+  a.x = fmaf(w, x.x, a.x); a.y = fmaf(w, x.y, a.y);
+}
+template <typename T>
+__device__ __forceinline__ void store_out(T* dst, const float4 a, float f) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(a.x * f, a.y * f), pack2<T>(a.z * f, a.w * f));
+}
+template <typename T>
+__device__ __forceinline__ void store_out(T* dst, const float2 a, float f) {
+  *reinterpret_cast<uint32_t*>(dst) = pack2<T>(a.x * f, a.y * f);
+}
+
+template <int D, typename T, bool F8, int NT>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const PageAttnParams p) {
+  using Z = Shape<D, F8, NT>;
+  using M = typename std::conditional<F8, __half, T>::type;  // operand type of the products
+  // f16 weights use the exponents above 1: with 2^11 for the running maximum, what is below
+  // f16's smallest step is below 2^-36 of it
+  constexpr float kShift = std::is_same<M, __half>::value ? 11.f : 0.f;
+  using V4 = typename Vec<D>::type;
+  constexpr int VL = D / 32;  // floats of V4
+  extern __shared__ __align__(128) char smem[];
+  __shared__ long long scan_sum[kWarps];
+  __shared__ int start_row[kWarps];
+  __shared__ long long start_in[kWarps];
+  __shared__ int2 meta[kWarps][Z::S];  // a stage's token mask; row, unit of the row and flags in 12 + 12 + 4 bits
+  __shared__ Part parts[2 * kWarps];
+  __shared__ int s_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g8 = lane >> 2, t4 = lane & 3;
+  const int U = p.Hkv * p.n_chunks;
+
+  // a row's visible tokens: x in [0, n) is token x (x < lo) or x + gap, or token x % page of
+  // selected page x / page
+  auto row_len = [&](int r) {
+    const int len = __ldg(p.kv_len + r);
+    return len >= -1 && (long long)len <= (long long)p.W * p.page ? len : -2;
+  };
+  auto div_page = [&](int n) { return (int)((__umulhi((uint32_t)n, p.div_mul) + (uint32_t)n) >> p.div_shift); };
+  auto visible = [&](int len, int& lo, int& gap) {
+    if (p.sel) {
+      lo = gap = 0;
+      return min(p.topk, div_page(len) + (div_page(len) * p.page < len ? 1 : 0)) * p.page;
     }
-    const int pg = p.table[r * p.table_stride + tok / p.page];
-    if (pg < 0 || pg >= p.n_pages) {
-      if (p.err && lane == 0) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
+    lo = p.window > 0 ? min(p.sink, len) : len;
+    gap = p.window > 0 ? max(0, len - p.window - lo) : 0;
+    return len - gap;
+  };
+  auto row_tiles = [&](int len) {  // a row without visible tokens still gets its outputs
+    if (len < 0) return 0;
+    int lo, gap;
+    return max(1, (visible(len, lo, gap) + Z::TT - 1) / Z::TT);
+  };
+
+  // ---- the line: total length, and where this block's warps begin
+  const int per = (p.R + kThreads - 1) / kThreads;
+  const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int len = row_len(r);
+    if (len == -2 && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_OFFSETS);
+    mine += row_tiles(len);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scan_sum[warp] = incl;
+  if (tid < 2 * kWarps) parts[tid].tb = parts[tid].te = 0;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += scan_sum[w];
+    total += scan_sum[w];
+  }
+  total *= U;
+  if (total == 0) return;
+  const long long n_share = min((long long)gridDim.x * kWarps, (total + kMinTiles - 1) / kMinTiles);
+  Shares sh;
+  sh.q = total / n_share;
+  sh.rem = total - sh.q * n_share;
+#pragma unroll 1
+  for (int w = 0; w < kWarps; ++w) {
+    const long long ww = (long long)blockIdx.x * kWarps + w;
+    if (ww >= n_share) break;
+    const long long x = sh.begin(ww);
+    if (x >= before * U && x < (before + mine) * U) {
+      long long at = before * U;
+      for (int r = r0; r < r1; ++r) {
+        const long long n = (long long)row_tiles(row_len(r)) * U;
+        if (x < at + n) {
+          start_row[w] = r;
+          start_in[w] = x - at;
+          break;
+        }
+        at += n;
+      }
+    }
+  }
+  __syncthreads();
+
+  const long long my_w = (long long)blockIdx.x * kWarps + warp;
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * Z::WARP);
+  int count = my_w < n_share ? (int)(sh.q + (my_w < sh.rem ? 1 : 0)) : 0;
+  if (count > 0) {
+    // ---- cursor: the next tile to look up
+    int cr = start_row[warp], len = row_len(cr), lo, gap, n_vis = visible(len, lo, gap);
+    int tiles = row_tiles(len);
+    int cu = (int)(start_in[warp] / tiles), ct = (int)(start_in[warp] - (long long)cu * tiles);
+    int todo = count;  // tiles not yet looked up
+    bool first = true;
+    const long long line0 = sh.begin(my_w);
+    const int tok_lane = lane & (Z::TT - 1);
+
+    int nx_page = -1, nx_off = 0, nx_r = 0, nx_u = 0, nx_flags = 0;
+    bool nx_want = false;
+    // flags: 1 the share's piece of a unit begins, 2 it ends, 4 the unit begins, 8 the unit ends
+    auto lookup = [&]() {
+      nx_r = cr;
+      nx_u = cu;
+      nx_flags = (first || ct == 0 ? 1 : 0) | (todo == 1 || ct == tiles - 1 ? 2 : 0) | (ct == 0 ? 4 : 0) |
+                 (ct == tiles - 1 ? 8 : 0);
+      first = false;
+      const int x = ct * Z::TT + tok_lane;
+      nx_want = x < n_vis;
+      nx_page = -1;
+      if (nx_want) {
+        int j, tok;
+        if (p.sel) {
+          const int e = div_page(x);
+          j = __ldg(p.sel + ((long long)cr * p.Hkv + cu / p.n_chunks) * p.topk + e);
+          nx_off = x - e * p.page;
+          if (j < 0 || j >= p.W) {
+            if (j != -1 && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
+            nx_want = false;
+          } else {
+            tok = j * p.page + nx_off;
+            nx_want = tok < len;
+          }
+        } else {
+          tok = x < lo ? x : x + gap;
+          j = div_page(tok);
+          nx_off = tok - j * p.page;
+        }
+        if (nx_want) nx_page = __ldg(p.table + cr * p.table_stride + j);
+      }
+      --todo;
+      if (++ct == tiles) {
+        ct = 0;
+        if (++cu == U && todo > 0) {
+          cu = 0;
+          // the next row with tiles: there is one, the line has `todo` more
+          int base = cr + 1;
+          while (base < p.R) {
+            const int l = base + lane < p.R ? row_len(base + lane) : -1;
+            const unsigned b = __ballot_sync(0xFFFFFFFFu, l >= 0);
+            if (b) {
+              cr = base + __ffs(b) - 1;
+              break;
+            }
+            base += 32;
+          }
+          len = row_len(cr);
+          n_vis = visible(len, lo, gap);
+          tiles = row_tiles(len);
+        }
+      }
+    };
+    auto issue = [&](int stage) {
+      const bool ok = nx_want && nx_page >= 0 && nx_page < p.n_pages;
+      if (nx_want && !ok && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
+      const unsigned mask = __ballot_sync(0xFFFFFFFFu, ok) & (Z::TT == 32 ? 0xFFFFFFFFu : (1u << Z::TT) - 1u);
+      if (lane == 0) meta[warp][stage] = make_int2((int)mask, nx_r << 16 | nx_u << 4 | nx_flags);
+      const int h = nx_u / p.n_chunks;
+      const long long ko = ok ? nx_page * p.k_sb + nx_off * p.k_st : 0, vo = ok ? nx_page * p.v_sb + nx_off * p.v_st : 0;
+      const char* kb = p.k + h * p.k_sh;
+      const char* vb = p.v + h * p.v_sh;
+      const uint32_t dk = ring + (uint32_t)(stage * 2 * Z::TILE), dv = dk + Z::TILE;
+#pragma unroll
+      for (int i = 0; i < Z::TT * Z::CPR / 32; ++i) {
+        const int row = (i * 32 + lane) / Z::CPR, piece = lane % Z::CPR;
+        const long long rk = __shfl_sync(0xFFFFFFFFu, ko, row), rv = __shfl_sync(0xFFFFFFFFu, vo, row);
+        const int n = (mask >> row) & 1u ? 16 : 0;
+        const uint32_t at = piece_at<Z::RB>(row, piece);
+        cp_async16_zfill(dk + at, kb + rk + piece * 16, n);
+        cp_async16_zfill(dv + at, vb + rv + piece * 16, n);
+      }
+    };
+
+    lookup();
+#pragma unroll
+    for (int s = 0; s < Z::S - 1; ++s) {
+      if (s < count) {
+        issue(s);
+        if (todo > 0) lookup();
+      }
+      cp_async_commit();
+    }
+
+    // ---- consume
+    uint32_t qf[NT][D / 16][2];
+    float cs[NT][2];  // log2 score per product, for heads 2 t4 and 2 t4 + 1 of each 8
+    float m[NT][2], l[NT][2], acc[NT][D / 16][4];
+    int piece_t0 = 0, piece_n = 0;
+    bool unit_begin = false;
+    int stage = 0;
+    // ldmatrix row addresses: K pairs (tokens 0-7, 8-15) x (piece, next piece), V the other way round
+    const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_pc = lane >> 4;
+    const int v_row = (lane & 7) + (lane >> 4) * 8, v_pc = (lane >> 3) & 1;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      cp_async_wait<Z::S - 2>();
+      __syncwarp();
+      if (i + Z::S - 1 < count) {
+        issue(stage == 0 ? Z::S - 1 : stage - 1);
+        if (todo > 0) lookup();
+      }
+      cp_async_commit();
+      const int2 mt = meta[warp][stage];
+      const unsigned mask = (unsigned)mt.x;
+      const int r = mt.y >> 16, u = mt.y >> 4 & 4095, flags = mt.y & 15;
+      const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC;  // key head, first query head of the chunk
+      const int n_heads = min(Z::HC, p.G - hc0);
+      if (flags & 1) {
+        const T* q = reinterpret_cast<const T*>(p.q) + r * p.q_sb + (long long)(h * p.G + hc0) * p.q_sh;
+        const float c0 = p.scale_log2 * (F8 && p.ks ? __ldg(p.ks + h) : 1.f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int hd = nt * 8 + g8;
+          const bool in = hd < n_heads;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            // an 8-bit row's fragment has channels 16 c + 4 t4 ..+3, a 16-bit row's 16 c + 2 t4, +1, +8, +9
+            const int d0 = 16 * c + (F8 ? 4 * t4 : 2 * t4), d1 = d0 + (F8 ? 2 : 8);
+            qf[nt][c][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d0)) : 0u;
+            qf[nt][c][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d1)) : 0u;
+          }
+          float inv = 1.f;
+          if constexpr (F8 && std::is_same<T, __nv_bfloat16>::value) {
+            float big = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float2 x = unpack2<T>(qf[nt][c][e]);
+                big = fmaxf(big, fmaxf(fabsf(x.x), fabsf(x.y)));
+              }
+            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+            // big 2^f in [2^14, 2^15); |f| <= 126 so that both powers are normal numbers
+            const int ex = (int)(__float_as_uint(big) >> 23);
+            const int f = ex == 255 ? 0 : max(-113, min(126, 141 - ex));
+            const float mul = __uint_as_float((uint32_t)(127 + f) << 23);
+            inv = __uint_as_float((uint32_t)(127 - f) << 23);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float2 x = unpack2<T>(qf[nt][c][e]);
+                qf[nt][c][e] = pack2<__half>(x.x * mul, x.y * mul);
+              }
+          }
+          const float ch = c0 * inv;
+          cs[nt][0] = __shfl_sync(0xFFFFFFFFu, ch, 8 * t4);
+          cs[nt][1] = __shfl_sync(0xFFFFFFFFu, ch, 8 * t4 + 4);
+          m[nt][0] = m[nt][1] = -INFINITY;
+          l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][c][e] = 0.f;
+        }
+        piece_n = 0;
+        piece_t0 = i;
+        unit_begin = (flags & 4) != 0;
+      }
+      ++piece_n;
+      const uint32_t sk = ring + (uint32_t)(stage * 2 * Z::TILE), sv = sk + Z::TILE;
+
+      // ---- scores
+      float s[Z::MT][NT][4];
+#pragma unroll
+      for (int mt2 = 0; mt2 < Z::MT; ++mt2)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt2][nt][e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < Z::CPR; c += 2) {
+#pragma unroll
+        for (int mt2 = 0; mt2 < Z::MT; ++mt2) {
+          uint32_t a[4];
+          ldsm4(sk + piece_at<Z::RB>(mt2 * 16 + k_row, c + k_pc), a);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (F8) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                mma16816<M>(s[mt2][nt], e4m3x2_to_f16x2(a[2 * e]), e4m3x2_to_f16x2(a[2 * e + 1]),
+                            e4m3x2_to_f16x2(a[2 * e] >> 16), e4m3x2_to_f16x2(a[2 * e + 1] >> 16), qf[nt][c + e][0],
+                            qf[nt][c + e][1]);
+            } else {
+              mma16816<M>(s[mt2][nt], a[0], a[1], a[2], a[3], qf[nt][c / 2][0], qf[nt][c / 2][1]);
+            }
+          }
+        }
+      }
+      // ---- weights
+      float top[NT][2];
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[nt][e] = -INFINITY;
+#pragma unroll
+          for (int mt2 = 0; mt2 < Z::MT; ++mt2)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float& x = s[mt2][nt][2 * hf + e];
+              x = (mask >> (mt2 * 16 + hf * 8 + g8)) & 1u ? x * cs[nt][e] : -INFINITY;
+              top[nt][e] = fmaxf(top[nt][e], x);
+            }
+          over |= top[nt][e] > m[nt][e] + kSlack;
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(top[nt][e], m[nt][e]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+            const float a = exp2f(m[nt][e] - (x == -INFINITY ? 0.f : x));
+            m[nt][e] = x;
+            l[nt][e] *= a;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              acc[nt][c][e] *= a;
+              acc[nt][c][2 + e] *= a;
+            }
+          }
+      }
+      uint32_t ph[Z::MT][NT][2], pl[Z::MT][NT][2];  // B fragments: weights' values and remainders
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kShift;
+        const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kShift;
+#pragma unroll
+        for (int mt2 = 0; mt2 < Z::MT; ++mt2)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float p0 = ex2_approx(s[mt2][nt][2 * hf] - b0), p1 = ex2_approx(s[mt2][nt][2 * hf + 1] - b1);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            const uint32_t hi = pack2<M>(p0, p1);
+            const float2 b = unpack2<M>(hi);
+            ph[mt2][nt][hf] = movm_t(hi);
+            pl[mt2][nt][hf] = movm_t(pack2<M>(p0 - b.x, p1 - b.y));
+          }
+      }
+      // ---- outputs
+#pragma unroll
+      for (int c = 0; c < Z::CPR; c += 2) {
+#pragma unroll
+        for (int mt2 = 0; mt2 < Z::MT; ++mt2) {
+          uint32_t a[4];
+          ldsm4_t(sv + piece_at<Z::RB>(mt2 * 16 + v_row, c + v_pc), a);
+          if constexpr (F8) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // bytes (token, channel): (0,0) (0,1) (1,0) (1,1) -> (0,0) (1,0) (0,1) (1,1)
+              const uint32_t x = __byte_perm(a[e], 0, 0x3120), y = __byte_perm(a[2 + e], 0, 0x3120);
+              const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2_to_f16x2(x >> 16), a2 = e4m3x2_to_f16x2(y),
+                             a3 = e4m3x2_to_f16x2(y >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816<M>(acc[nt][c + e], a0, a1, a2, a3, ph[mt2][nt][0], ph[mt2][nt][1]);
+                mma16816<M>(acc[nt][c + e], a0, a1, a2, a3, pl[mt2][nt][0], pl[mt2][nt][1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<M>(acc[nt][c / 2], a[0], a[1], a[2], a[3], ph[mt2][nt][0], ph[mt2][nt][1]);
+              mma16816<M>(acc[nt][c / 2], a[0], a[1], a[2], a[3], pl[mt2][nt][0], pl[mt2][nt][1]);
+            }
+          }
+        }
+      }
+      if (flags & 2) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], o);
+        if (unit_begin && (flags & 8)) {  // the whole unit
+          const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
+          T* o = reinterpret_cast<T*>(p.o) + r * p.o_sb + (long long)(h * p.G + hc0) * p.o_sh;
+          float* lse = p.lse + (size_t)r * p.H + h * p.G + hc0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float f0 = l[nt][0] == 0.f ? 0.f : vs / l[nt][0], f1 = l[nt][1] == 0.f ? 0.f : vs / l[nt][1];
+            const int hd = nt * 8 + g8;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const uint32_t x = movm_t(pack2<T>(acc[nt][c][0] * f0, acc[nt][c][1] * f1));
+              const uint32_t y = movm_t(pack2<T>(acc[nt][c][2] * f0, acc[nt][c][3] * f1));
+              if (hd < n_heads) {
+                T* dst = o + hd * p.o_sh + 16 * c;
+                if constexpr (F8) {  // x: channels 4 t4, 4 t4 + 2; y: 4 t4 + 1, 4 t4 + 3
+                  *reinterpret_cast<uint2*>(dst + 4 * t4) =
+                      make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+                } else {
+                  *reinterpret_cast<uint32_t*>(dst + 2 * t4) = x;
+                  *reinterpret_cast<uint32_t*>(dst + 8 + 2 * t4) = y;
+                }
+              }
+            }
+            if (lane < 4) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (nt * 8 + 2 * lane + e < n_heads)
+                  lse[nt * 8 + 2 * lane + e] =
+                      l[nt][e] == 0.f ? -INFINITY : (m[nt][e] - kShift + log2f(l[nt][e])) * 0.69314718055994531f;
+            }
+          }
+        } else {
+          // a part: the share's first piece goes behind the rings, its last into this warp's ring (all read)
+          const bool is_first = i + 1 == piece_n;
+          const int slot = 2 * warp + (is_first ? 0 : 1);
+          float* po = is_first ? reinterpret_cast<float*>(smem + kWarps * Z::WARP + warp * Z::PART)
+                               : reinterpret_cast<float*>(smem + warp * Z::WARP);
+          __syncwarp();
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int hd = nt * 8 + 2 * t4;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int d = 16 * c + (F8 ? 2 * g8 + (e >> 1) : g8 + (e >> 1) * 8);
+                po[(hd + (e & 1)) * Z::LD + d] = acc[nt][c][e];
+              }
+            if (lane < 4) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                po[(nt * 8 + 2 * lane + e) * Z::LD + D] = m[nt][e];
+                po[(nt * 8 + 2 * lane + e) * Z::LD + D + 1] = l[nt][e];
+              }
+            }
+          }
+          if (lane == 0) {
+            // the piece's first tile within its unit: known from the share's start, or 0
+            const int tl = row_tiles(row_len(r));
+            const int tb = is_first ? (int)(start_in[warp] % tl) : 0;
+            Part& pt = parts[slot];
+            pt.r = r;
+            pt.u = u;
+            pt.tb = tb;
+            pt.te = tb + piece_n;
+            pt.tiles = tl;
+            pt.unit0 = line0 + piece_t0 - tb;
+          }
+        }
+      }
+      stage = stage + 1 == Z::S ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+  }
+  __syncthreads();
+
+  // ---- join the block's parts; units that go on in other blocks meet in the workspace
+  auto part_o = [&](int i) {
+    return reinterpret_cast<const float*>((i & 1) ? smem + (i >> 1) * Z::WARP : smem + kWarps * Z::WARP + (i >> 1) * Z::PART);
+  };
+  const int hcw = min(Z::HC, p.G);  // heads of a workspace part
+#pragma unroll 1
+  for (int i = 0; i < 2 * kWarps;) {
+    if (parts[i].te == 0) {
+      ++i;
       continue;
     }
-    const char* kr = p.k + pg * p.k_sb + (tok % p.page) * p.k_st + g * p.k_sh;
-    const char* vr = p.v + pg * p.v_sb + (tok % p.page) * p.v_st + g * p.v_sh;
-    float s = 0.f;
+    const Part a = parts[i];
+    int end = i + 1, te = a.te;
+    for (int j = i + 1; j < 2 * kWarps; ++j) {
+      if (parts[j].te == 0) continue;
+      if (parts[j].r != a.r || parts[j].u != a.u) break;
+      end = j + 1;
+      te = parts[j].te;
+    }
+    const int h = a.u / p.n_chunks, hc0 = (a.u - h * p.n_chunks) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
+    const bool whole = a.tb == 0 && te == a.tiles;
+    const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
+    T* o = reinterpret_cast<T*>(p.o) + a.r * p.o_sb + (long long)(h * p.G + hc0) * p.o_sh;
+    float* lse = p.lse + (size_t)a.r * p.H + h * p.G + hc0;
+    const size_t ws = (size_t)(2 * blockIdx.x + (a.tb == 0 ? 1 : 0)) * hcw;
+    for (int hd = warp; hd < n_heads; hd += kWarps) {
+      float top = -INFINITY, sum = 0.f;
+      for (int j = i; j < end; ++j)
+        if (parts[j].te) top = fmaxf(top, part_o(j)[hd * Z::LD + D]);
+      const float base = top == -INFINITY ? 0.f : top;
+      V4 x;
+      std::memset(&x, 0, sizeof(x));
+      for (int j = i; j < end; ++j) {
+        if (!parts[j].te) continue;
+        const float w = exp2f(part_o(j)[hd * Z::LD + D] - base);
+        sum = fmaf(w, part_o(j)[hd * Z::LD + D + 1], sum);
+        axpy(x, w, *reinterpret_cast<const V4*>(part_o(j) + hd * Z::LD + lane * VL));
+      }
+      if (whole) {
+        store_out(o + hd * p.o_sh + lane * VL, x, sum == 0.f ? 0.f : vs / sum);
+        if (lane == 0) lse[hd] = sum == 0.f ? -INFINITY : (base - kShift + log2f(sum)) * 0.69314718055994531f;
+      } else {
+        *reinterpret_cast<V4*>(p.ws_o + (ws + hd) * D + lane * VL) = x;
+        if (lane == 0) *reinterpret_cast<float2*>(p.ws_ml + (ws + hd) * 2) = make_float2(top, sum);
+      }
+    }
+    if (!whole) {
+      const int b0 = sh.warp_of(a.unit0) / kWarps, b1 = sh.warp_of(a.unit0 + a.tiles - 1) / kWarps;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(p.counters + b0, 1) == b1 - b0;
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        if (tid == 0) p.counters[b0] = 0;
+        const int n = b1 - b0 + 1;
+        for (int hd = warp; hd < n_heads; hd += kWarps) {
+          auto ml = [&](int j) {
+            return __ldcg(reinterpret_cast<const float2*>(p.ws_ml + ((size_t)(2 * (b0 + j) + (j == 0 ? 1 : 0)) * hcw + hd) * 2));
+          };
+          float top = -INFINITY;
+          for (int j = lane; j < n; j += 32) top = fmaxf(top, ml(j).x);
 #pragma unroll
-    for (int i = 0; i < PL; ++i) s += qr[i] * elem<T, E4M3>(kr, lane + 32 * i);
+          for (int q = 16; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, q));
+          const float base = top == -INFINITY ? 0.f : top;
+          V4 x;
+          std::memset(&x, 0, sizeof(x));
+          float sum = 0.f;
+          for (int j0 = 0; j0 < n; j0 += 32) {
+            const float2 v = j0 + lane < n ? ml(j0 + lane) : make_float2(-INFINITY, 0.f);
+            const float wl = exp2f(v.x - base);
+            sum = fmaf(wl, v.y, sum);
+            const int jn = min(32, n - j0);
+#pragma unroll 8
+            for (int j = 0; j < jn; ++j) {
+              const float w = __shfl_sync(0xFFFFFFFFu, wl, j);
+              const int b = b0 + j0 + j;
+              axpy(x, w, __ldcg(reinterpret_cast<const V4*>(
+                             p.ws_o + ((size_t)(2 * b + (b == b0 ? 1 : 0)) * hcw + hd) * D + lane * VL)));
+            }
+          }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    s *= ks;
-    const float mn = fmaxf(m, s), ms = mn == -INFINITY ? 0.f : mn;
-    const float a = exp2f(m - ms), w = exp2f(s - ms);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) acc[i] = acc[i] * a + w * elem<T, E4M3>(vr, lane + 32 * i);
+          for (int q = 16; q > 0; q >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, q);
+          store_out(o + hd * p.o_sh + lane * VL, x, sum == 0.f ? 0.f : vs / sum);
+          if (lane == 0) lse[hd] = sum == 0.f ? -INFINITY : (base - kShift + log2f(sum)) * 0.69314718055994531f;
+        }
+      }
+      __syncthreads();  // s_last has been read
+    }
+    i = end;
   }
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < PL; ++i) sm_o[warp][lane + 32 * i] = acc[i];
-  __syncthreads();
-  float M = -INFINITY, L = 0.f;
-#pragma unroll
-  for (int w = 0; w < kSimpleWarps; ++w) M = fmaxf(M, sm_m[w]);
-  const float Ms = M == -INFINITY ? 0.f : M;
-#pragma unroll
-  for (int w = 0; w < kSimpleWarps; ++w) L += sm_l[w] * exp2f(sm_m[w] - Ms);
-  T* o = reinterpret_cast<T*>(p.o) + r * p.o_sb + h * p.o_sh;
-  for (int c = threadIdx.x; c < D; c += kSimpleWarps * 32) {
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < kSimpleWarps; ++w) t += sm_o[w][c] * exp2f(sm_m[w] - Ms);
-    o[c] = from_float<T>(L == 0.f ? 0.f : t / L * vs);
-  }
-  if (threadIdx.x == 0) p.lse[(size_t)r * p.H + h] = L == 0.f ? -INFINITY : (Ms + log2f(L)) * 0.69314718055994531f;
 }
 
-template <int D, typename T, bool E4M3>
-cudaError_t launch(const PageAttnParams& p, cudaStream_t st) {
-  page_attn_kernel<D, T, E4M3><<<(unsigned)(p.R * p.H), kSimpleWarps * 32, 0, st>>>(p);
+// ---------------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------------
+template <int D, typename T, bool F8, int NT>
+cudaError_t launch(const PageAttnParams& p, int blocks, cudaStream_t st) {
+  using Z = Shape<D, F8, NT>;
+  auto fn = page_attn_kernel<D, T, F8, NT>;
+  const cudaError_t rc = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
+  if (rc != cudaSuccess) return rc;
+  fn<<<(unsigned)blocks, kThreads, Z::SMEM, st>>>(p);
   return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_d(const PageAttnParams& p, int q_dtype, int kv_dtype, cudaStream_t st) {
-  if (kv_dtype == VKV_E4M3)
-    return q_dtype == VKV_BF16 ? launch<D, __nv_bfloat16, true>(p, st) : launch<D, __half, true>(p, st);
-  return q_dtype == VKV_BF16 ? launch<D, __nv_bfloat16, false>(p, st) : launch<D, __half, false>(p, st);
+template <int D, typename T, bool F8>
+cudaError_t launch_nt(const PageAttnParams& p, int blocks, cudaStream_t st) {
+  return p.G <= 8 ? launch<D, T, F8, 1>(p, blocks, st) : launch<D, T, F8, 2>(p, blocks, st);
 }
+
+template <int D>
+cudaError_t launch_d(const PageAttnParams& p, int q_dtype, int kv_dtype, int blocks, cudaStream_t st) {
+  if (kv_dtype == VKV_E4M3)
+    return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, true>(p, blocks, st) : launch_nt<D, __half, true>(p, blocks, st);
+  return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, false>(p, blocks, st) : launch_nt<D, __half, false>(p, blocks, st);
+}
+
+// Bytes of the counters and of one block's two workspace parts.
+constexpr size_t kCounterBytes = (kMaxBlocks * sizeof(int) + 255) / 256 * 256;
+size_t part_bytes(int G, int d) { return (size_t)2 * std::min(G, G <= 8 ? 8 : 16) * (d + 2) * sizeof(float); }
 
 }  // namespace
 }  // namespace vkv
@@ -147,7 +794,10 @@ using namespace vkv;
 
 extern "C" size_t vkv_page_attn_workspace_size(int32_t H, int32_t Hkv, int32_t d) {
   if (H < 1 || Hkv < 1 || H % Hkv || (d != 64 && d != 128)) return 0;
-  return 256;
+  const int n_sm = device_sm_count(nullptr);
+  if (n_sm <= 0) return 0;
+  const int blocks = std::min(kMaxBlocks, kBlocksPerSm * n_sm);
+  return (kCounterBytes + blocks * part_bytes(H / Hkv, d) + 255) / 256 * 256;
 }
 
 extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t stream) {
@@ -158,10 +808,10 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   if (a->R < 1 || a->R > VKV_PAGE_MAX_ROWS || a->H < 1 || a->Hkv < 1 || a->H % a->Hkv || a->page < 1 ||
       a->n_pages < 1 || a->W < 1 || a->sink < 0 || a->window < 0 || a->table_stride < a->W)
     return VKV_ERR_SHAPE;
-  if (!(a->scale > 0.f) || a->scale > 3.0e38f) return VKV_ERR_SHAPE;
+  if (!(a->scale > 0.f) || a->scale > 2.0e38f) return VKV_ERR_SHAPE;
   if (a->sel ? (a->topk < 1 || a->window != 0) : a->topk != 0) return VKV_ERR_SHAPE;
-  if ((long long)a->R * a->W > INT_MAX || (long long)a->W * a->page > INT_MAX || a->H > 4096 ||
-      (long long)a->topk * a->page > INT_MAX)
+  if ((long long)a->R * a->W > INT_MAX || (long long)a->W * a->page > INT_MAX - 64 || a->H > 4096 ||
+      (long long)a->topk * a->page > INT_MAX - 64)
     return VKV_ERR_UNSUPPORTED;
   if (a->kv_dtype != VKV_E4M3 && (a->k_scale || a->v_scale)) return VKV_ERR_UNSUPPORTED;
   if (!a->q.ptr || !a->o.ptr || !a->k.ptr || !a->v.ptr || !a->table || !a->kv_len || !a->lse) return VKV_ERR_NULL;
@@ -170,8 +820,8 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   if (!page_tensor_aligned(q, a->q_dtype) || !page_tensor_aligned(o, a->q_dtype) ||
       !page_tensor_aligned(a->k, a->kv_dtype) || !page_tensor_aligned(a->v, a->kv_dtype))
     return VKV_ERR_ALIGN;
-  int dev = 0;
-  if (device_sm_count(&dev) <= 0) return VKV_ERR_CUDA;
+  const int n_sm = device_sm_count(nullptr);
+  if (n_sm <= 0) return VKV_ERR_CUDA;
   const size_t need = vkv_page_attn_workspace_size(a->H, a->Hkv, a->d);
   if (!a->workspace || a->workspace_bytes < need) return VKV_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return VKV_ERR_ALIGN;
@@ -179,6 +829,10 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   std::memset(&p, 0, sizeof(p));
   p.R = a->R; p.H = a->H; p.Hkv = a->Hkv; p.G = a->H / a->Hkv;
   p.page = a->page; p.n_pages = a->n_pages; p.W = a->W; p.sink = a->sink; p.window = a->window; p.topk = a->topk;
+  while ((1ll << p.div_shift) < a->page) ++p.div_shift;
+  p.div_mul = (uint32_t)((((1ull << p.div_shift) - (uint32_t)a->page) << 32) / (uint32_t)a->page + 1);
+  const int hc = p.G <= 8 ? 8 : 16;
+  p.n_chunks = (p.G + hc - 1) / hc;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   p.q = a->q.ptr; p.q_sb = a->q.sb; p.q_sh = a->q.sh;
   p.o = a->o.ptr; p.o_sb = a->o.sb; p.o_sh = a->o.sh;
@@ -192,9 +846,20 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   p.sel = a->sel;
   p.ks = a->k_scale; p.vs = a->v_scale;
   p.lse = a->lse;
+  const int all = std::min(kMaxBlocks, kBlocksPerSm * n_sm);
+  p.counters = reinterpret_cast<int*>(a->workspace);
+  p.ws_ml = reinterpret_cast<float*>(reinterpret_cast<char*>(a->workspace) + kCounterBytes);
+  p.ws_o = p.ws_ml + (size_t)2 * all * std::min(p.G, hc) * 2;
   p.err = a->err_word;
+  // no more blocks than the longest rows that the table allows could fill
+  const int tt = a->d * e == 256 ? 16 : 32;
+  const long long most = a->sel ? std::min<long long>((long long)a->topk * a->page, (long long)a->W * a->page)
+                         : a->window > 0 ? std::min<long long>((long long)a->sink + a->window, (long long)a->W * a->page)
+                                         : (long long)a->W * a->page;
+  const long long tiles = ((most + tt - 1) / tt) * a->R * a->Hkv * p.n_chunks;
+  const int blocks = (int)std::min<long long>(all, (tiles + kMinTiles * kWarps - 1) / (kMinTiles * kWarps));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t rc = a->d == 128 ? launch_d<128>(p, a->q_dtype, a->kv_dtype, st)
-                                     : launch_d<64>(p, a->q_dtype, a->kv_dtype, st);
+  const cudaError_t rc = a->d == 128 ? launch_d<128>(p, a->q_dtype, a->kv_dtype, blocks, st)
+                                     : launch_d<64>(p, a->q_dtype, a->kv_dtype, blocks, st);
   return rc == cudaSuccess ? VKV_OK : VKV_ERR_CUDA;
 }
