@@ -55,6 +55,21 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// n / d for 0 <= n < 2^31 by a multiplication: (umulhi(n, mul) + n) >> shift, with
+// 2^shift >= d the next power of two and mul = floor(2^32 (2^shift - d) / d) + 1
+// (Granlund and Montgomery, Division by Invariant Integers using Multiplication, 1994).
+struct FastDiv {
+  uint32_t mul, shift;
+  __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+inline FastDiv fast_div(int d) {
+  FastDiv f;
+  f.shift = 0;
+  while ((1ll << f.shift) < d) ++f.shift;
+  f.mul = (uint32_t)((((1ull << f.shift) - (uint32_t)d) << 32) / (uint32_t)d + 1);
+  return f;
+}
+
 // Bytes of one element.
 inline int dtype_bytes(int dt) { return dt == VKV_E4M3 ? 1 : 2; }
 

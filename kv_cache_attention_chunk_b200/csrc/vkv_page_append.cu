@@ -57,21 +57,27 @@ __device__ __forceinline__ void store_chunk(char* dst, const uint4 x, float scal
   }
 }
 
-// Eight stored values of a cache row.
-template <typename IN, bool E4M3>
-__device__ __forceinline__ void load_chunk(const char* src, float* val) {
-  if constexpr (E4M3) {
-    const uint2 u = *reinterpret_cast<const uint2*>(src);
-    const uint32_t w[2] = {u.x, u.y};
+// Eight stored values of a cache row: as they lie there, and as fp32.
+template <bool E4M3>
+struct Raw { using type = uint4; };
+template <>
+struct Raw<true> { using type = uint2; };
+template <typename IN>
+__device__ __forceinline__ void add_raw(const uint4 x, float* acc) {
+  float f[8];
+  unpack8<IN>(x, f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t h2 = e4m3x2_to_f16x2(w[e >> 1] >> (16 * (e & 1)));
-      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-      val[2 * e] = p.x;
-      val[2 * e + 1] = p.y;
-    }
-  } else {
-    unpack8<IN>(*reinterpret_cast<const uint4*>(src), val);
+  for (int e = 0; e < 8; ++e) acc[e] += f[e];
+}
+template <typename IN>
+__device__ __forceinline__ void add_raw(const uint2 x, float* acc) {
+  const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t h2 = e4m3x2_to_f16x2(w[e >> 1] >> (16 * (e & 1)));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    acc[2 * e] += v.x;
+    acc[2 * e + 1] += v.y;
   }
 }
 
@@ -112,80 +118,84 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   }
 }
 
-// With means: a CTA (128 threads) takes the runs that start among `slab` consecutive
-// tokens, for one head.  A run is a page's tokens of this call (consecutive slots of one
-// page).  The CTA's row groups (D/8 lanes each, one row per group and pass) first add the
-// page's earlier rows, read from the cache, then copy the run's rows and add what they
-// store; the groups' sums meet in shared memory, in a fixed order.
-constexpr int kMeanThreads = 128;
+// With means: a warp takes the runs that start among `slab` (<= 32) consecutive tokens, for
+// one head; the block's warps take neighbouring heads, whose rows lie side by side.  A run is
+// a page's tokens of this call (consecutive slots of one page).  The warp's lane groups (D/8
+// lanes each, one row per group and load, kRun loads in flight) first add the page's earlier
+// rows, read from the cache, then copy the run's rows and add what they store; the groups'
+// sums meet by shuffles, in a fixed order.  A run is never split, so pages of thousands of
+// tokens leave most of the GPU idle.
+constexpr int kMeanWarps = 4;
+constexpr int kRun = 8;
 
 template <int D, typename IN, bool E4M3>
-__global__ void __launch_bounds__(kMeanThreads) append_mean_kernel(const AppendParams p, int slab) {
+__global__ void __launch_bounds__(kMeanWarps * 32, 4) append_mean_kernel(const AppendParams p, int slab) {
   constexpr int CPR = D / 8;
-  constexpr int GROUPS = kMeanThreads / CPR;
+  constexpr int GROUPS = 32 / CPR;
   constexpr int OB = E4M3 ? 8 : 16;
-  constexpr int U = 4;  // rows of a thread in flight
-  __shared__ float part[GROUPS][D];
-  const int h = blockIdx.y;
-  const int c = threadIdx.x % CPR, g = threadIdx.x / CPR;
+  const int lane = threadIdx.x & 31;
+  const int h = blockIdx.y * kMeanWarps + (threadIdx.x >> 5);
+  if (h >= p.Hkv) return;
+  const int c = lane % CPR, g = lane / CPR;
   const float ks = E4M3 && p.ks ? p.ks[h] : 1.f, vs = E4M3 && p.vs ? p.vs[h] : 1.f;
-  const long long i_end = min((long long)p.T, ((long long)blockIdx.x + 1) * slab);
-  for (long long i = (long long)blockIdx.x * slab; i < i_end; ++i) {
-    const long long s0 = p.slot[i];
-    if (s0 < 0) continue;
-    if (s0 >= p.n_slots) {
-      if (p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
-      continue;
-    }
-    const long long pg = s0 / p.page;
-    const int off = (int)(s0 - pg * p.page);
-    if (i > 0 && off > 0 && p.slot[i - 1] == s0 - 1) continue;  // inside a run that started before
-    // the run's length: consecutive slots up to the page's end
+  const long long i0 = (long long)blockIdx.x * slab;
+  const int n_tok = (int)min((long long)slab, p.T - i0);
+  const long long s = lane < n_tok ? p.slot[i0 + lane] : -1;
+  const long long prev = lane < n_tok && i0 + lane > 0 ? p.slot[i0 + lane - 1] : -2;
+  const bool bad = s >= p.n_slots;
+  if (bad && h == 0 && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
+  const bool ok = s >= 0 && !bad;
+  const long long page_l = ok ? (s >> 32 ? s / p.page : (long long)((uint32_t)s / (uint32_t)p.page)) : 0;
+  const int off_l = ok ? (int)(s - page_l * p.page) : 0;
+  unsigned starts = __ballot_sync(0xFFFFFFFFu, ok && !(off_l > 0 && prev == s - 1));
+#pragma unroll 1
+  for (; starts; starts &= starts - 1) {
+    const int b = __ffs(starts) - 1;
+    const long long i = i0 + b, s0 = __shfl_sync(0xFFFFFFFFu, s, b), pg = __shfl_sync(0xFFFFFFFFu, page_l, b);
+    const int off = __shfl_sync(0xFFFFFFFFu, off_l, b);
+    // the run's length: consecutive slots up to the page's end, in the slab and behind it
     const int most = (int)min((long long)(p.page - off), (long long)p.T - i);
-    int n = 1;
-    for (int t0 = 1; t0 < most; t0 += 32) {
-      const int t = t0 + (threadIdx.x & 31);
-      const bool in = t < most && p.slot[i + t] == s0 + t;
-      const unsigned b = __ballot_sync(0xFFFFFFFFu, in);
-      const int run = __ffs(~b) == 0 ? 32 : __ffs(~b) - 1;
-      n += run;
-      if (run < 32) break;
+    const unsigned in = __ballot_sync(0xFFFFFFFFu, lane >= b && lane - b < most && s == s0 + (lane - b)) >> b;
+    int n = in == 0xFFFFFFFFu ? 32 : __ffs(~in) - 1;
+    if (b + n == n_tok) {
+      while (n < most) {
+        const unsigned more = __ballot_sync(0xFFFFFFFFu, n + lane < most && p.slot[i + n + lane] == s0 + n + lane);
+        const int run = more == 0xFFFFFFFFu ? 32 : __ffs(~more) - 1;
+        n += run;
+        if (run < 32) break;
+      }
     }
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
     const char* kp = p.k + pg * p.k_sb + h * p.k_sh + c * OB;
-    for (int r0 = g; r0 < off; r0 += GROUPS * U) {  // the page's earlier rows
-      float f[U][8];
+    for (int r0 = g; r0 < off; r0 += GROUPS * kRun) {  // the page's earlier rows
+      typename Raw<E4M3>::type x[kRun];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < kRun; ++u) {
         const int r = r0 + u * GROUPS;
-        if (r < off) {
-          load_chunk<IN, E4M3>(kp + r * p.k_st, f[u]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[u][e] = 0.f;
-        }
+        if (r < off) x[u] = *reinterpret_cast<const typename Raw<E4M3>::type*>(kp + r * p.k_st);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += f[u][e];
+      for (int u = 0; u < kRun; ++u)
+        if (r0 + u * GROUPS < off) add_raw<IN>(x[u], acc);
     }
     char* kd = p.k + pg * p.k_sb + off * p.k_st + h * p.k_sh + c * OB;
     char* vd = p.v + pg * p.v_sb + off * p.v_st + h * p.v_sh + c * OB;
-    for (int r0 = g; r0 < n; r0 += GROUPS * U) {
-      uint4 kx[U], vx[U];
+    const uint4* kn = p.kn + i * p.kn_st + h * p.kn_sh + c;
+    const uint4* vn = p.vn + i * p.vn_st + h * p.vn_sh + c;
+    for (int r0 = g; r0 < n; r0 += GROUPS * kRun) {
+      uint4 kx[kRun], vx[kRun];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < kRun; ++u) {
         const int r = r0 + u * GROUPS;
         if (r < n) {
-          kx[u] = __ldcs(p.kn + (i + r) * p.kn_st + h * p.kn_sh + c);
-          vx[u] = __ldcs(p.vn + (i + r) * p.vn_st + h * p.vn_sh + c);
+          kx[u] = __ldcs(kn + r * p.kn_st);
+          vx[u] = __ldcs(vn + r * p.vn_st);
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < kRun; ++u) {
         const int r = r0 + u * GROUPS;
         if (r < n) {
           float f[8];
@@ -196,16 +206,17 @@ __global__ void __launch_bounds__(kMeanThreads) append_mean_kernel(const AppendP
         }
       }
     }
-    __syncthreads();  // the previous run's sums have been read
 #pragma unroll
-    for (int e = 0; e < 8; ++e) part[g][c * 8 + e] = acc[e];
-    __syncthreads();
-    const float rows = (float)(off + n);
-    for (int x = threadIdx.x; x < D; x += kMeanThreads) {
-      float t = 0.f;
+    for (int o = CPR; o < 32; o <<= 1)
 #pragma unroll
-      for (int gg = 0; gg < GROUPS; ++gg) t += part[gg][x];
-      p.kbar[(pg * p.Hkv + h) * D + x] = __fdiv_rn(t, rows) * ks;
+      for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], o);
+    if (g == 0) {
+      const float rows = (float)(off + n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = __fdiv_rn(acc[e], rows) * ks;
+      float4* dst = reinterpret_cast<float4*>(p.kbar + (pg * p.Hkv + h) * D + c * 8);
+      dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
     }
   }
 }
@@ -213,11 +224,10 @@ __global__ void __launch_bounds__(kMeanThreads) append_mean_kernel(const AppendP
 template <int D, typename IN, bool E4M3>
 cudaError_t launch(const AppendParams& p, int n_sm, cudaStream_t st) {
   if (p.kbar) {
-    // few tokens: one run start per CTA; many: as many as leave about 16 CTAs per SM
-    const long long want = 16ll * n_sm;
-    const int slab = (int)std::min<long long>(32, std::max<long long>(1, (long long)p.T * p.Hkv / want));
-    const dim3 grid((unsigned)((p.T + slab - 1) / slab), (unsigned)p.Hkv);
-    append_mean_kernel<D, IN, E4M3><<<grid, kMeanThreads, 0, st>>>(p, slab);
+    // few tokens: one run start per warp; many: as many as leave about 32 warps per SM
+    const int slab = (int)std::min<long long>(32, std::max<long long>(1, (long long)p.T * p.Hkv / (32ll * n_sm)));
+    const dim3 grid((unsigned)((p.T + slab - 1) / slab), (unsigned)((p.Hkv + kMeanWarps - 1) / kMeanWarps));
+    append_mean_kernel<D, IN, E4M3><<<grid, kMeanWarps * 32, 0, st>>>(p, slab);
   } else {
     const int cols = p.Hkv * (D / 8), n_cb = (cols + 255) / 256;
     const int width = (((cols + n_cb - 1) / n_cb) + 31) / 32 * 32;

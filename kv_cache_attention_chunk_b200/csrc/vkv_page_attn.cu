@@ -25,6 +25,7 @@
 // 16-bit parts (value and remainder), so that no rounding of P to 16 bits is left; sums and
 // outputs are fp32.  The running maximum only moves when a score exceeds it by 2^4.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstring>
 #include <type_traits>
@@ -46,7 +47,7 @@ constexpr int kMinTiles = VKV_PAGE_MIN_TILES;  // least share of a warp
 
 struct PageAttnParams {
   int R, H, Hkv, G, page, n_pages, W, sink, window, topk;
-  uint32_t div_mul, div_shift;  // n / page = (umulhi(n, mul) + n) >> shift, n < 2^31
+  FastDiv by_page;
   int n_chunks;                 // chunks of query heads per key head
   float scale_log2;
   const void* q;
@@ -162,6 +163,21 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
     return (uint32_t)(row * RB + ((piece ^ ((row >> 1) & 3)) << 4));
 }
 
+// x / y for x >= 0, y > 0; 64-bit division only where it is needed (it takes hundreds of cycles).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+  return x / y;
+}
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 struct Part {  // what a warp leaves of a cut unit; valid: te > tb
   int r, u, tb, te, tiles;
   long long unit0;  // the unit's first tile on the line
@@ -173,7 +189,7 @@ struct Shares {
   __device__ __forceinline__ long long begin(long long w) const { return w * q + min(w, rem); }
   __device__ __forceinline__ int warp_of(long long x) const {
     const long long cut = rem * (q + 1);
-    return (int)(x < cut ? x / (q + 1) : rem + (x - cut) / q);
+    return (int)(x < cut ? quotient(x, q + 1) : rem + quotient(x - cut, q));
   }
 };
 
@@ -209,9 +225,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
   using V4 = typename Vec<D>::type;
   constexpr int VL = D / 32;  // floats of V4
   extern __shared__ __align__(128) char smem[];
-  __shared__ long long scan_sum[kWarps];
-  __shared__ int start_row[kWarps];
-  __shared__ long long start_in[kWarps];
   __shared__ int2 meta[kWarps][Z::S];  // a stage's token mask; row, unit of the row and flags in 12 + 12 + 4 bits
   __shared__ Part parts[2 * kWarps];
   __shared__ int s_last;
@@ -226,11 +239,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
     const int len = __ldg(p.kv_len + r);
     return len >= -1 && (long long)len <= (long long)p.W * p.page ? len : -2;
   };
-  auto div_page = [&](int n) { return (int)((__umulhi((uint32_t)n, p.div_mul) + (uint32_t)n) >> p.div_shift); };
   auto visible = [&](int len, int& lo, int& gap) {
     if (p.sel) {
       lo = gap = 0;
-      return min(p.topk, div_page(len) + (div_page(len) * p.page < len ? 1 : 0)) * p.page;
+      return min(p.topk, p.by_page(len) + (p.by_page(len) * p.page < len ? 1 : 0)) * p.page;
     }
     lo = p.window > 0 ? min(p.sink, len) : len;
     gap = p.window > 0 ? max(0, len - p.window - lo) : 0;
@@ -242,67 +254,60 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
     return max(1, (visible(len, lo, gap) + Z::TT - 1) / Z::TT);
   };
 
-  // ---- the line: total length, and where this block's warps begin
-  const int per = (p.R + kThreads - 1) / kThreads;
-  const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
+  // ---- the line: its length and where this warp's share begins; every warp finds that by
+  // itself (each lane adds up a run of rows), so that none waits for another
+  const int per = (p.R + 31) / 32;
+  const int r0 = min(p.R, lane * per), r1 = min(p.R, r0 + per);
   long long mine = 0;
+  int len = -1;
   for (int r = r0; r < r1; ++r) {
-    const int len = row_len(r);
-    if (len == -2 && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_OFFSETS);
+    len = row_len(r);
+    if (len == -2 && p.err && blockIdx.x == 0 && warp == 0) atomicCAS(p.err, 0, VKV_DEVERR_BAD_OFFSETS);
     mine += row_tiles(len);
   }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) scan_sum[warp] = incl;
-  if (tid < 2 * kWarps) parts[tid].tb = parts[tid].te = 0;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += scan_sum[w];
-    total += scan_sum[w];
-  }
-  total *= U;
+  long long before = warp_scan(mine, lane);
+  const long long total = __shfl_sync(0xFFFFFFFFu, before, 31) * U;
+  before -= mine;
   if (total == 0) return;
   const long long n_share = min((long long)gridDim.x * kWarps, (total + kMinTiles - 1) / kMinTiles);
+  if ((long long)blockIdx.x * kWarps >= n_share) return;
   Shares sh;
-  sh.q = total / n_share;
+  sh.q = quotient(total, n_share);
   sh.rem = total - sh.q * n_share;
-#pragma unroll 1
-  for (int w = 0; w < kWarps; ++w) {
-    const long long ww = (long long)blockIdx.x * kWarps + w;
-    if (ww >= n_share) break;
-    const long long x = sh.begin(ww);
-    if (x >= before * U && x < (before + mine) * U) {
-      long long at = before * U;
-      for (int r = r0; r < r1; ++r) {
-        const long long n = (long long)row_tiles(row_len(r)) * U;
-        if (x < at + n) {
-          start_row[w] = r;
-          start_in[w] = x - at;
-          break;
-        }
-        at += n;
-      }
-    }
-  }
-  __syncthreads();
-
   const long long my_w = (long long)blockIdx.x * kWarps + warp;
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * Z::WARP);
+  if (lane < 2) parts[2 * warp + lane].te = 0;
   int count = my_w < n_share ? (int)(sh.q + (my_w < sh.rem ? 1 : 0)) : 0;
   if (count > 0) {
-    // ---- cursor: the next tile to look up
-    int cr = start_row[warp], len = row_len(cr), lo, gap, n_vis = visible(len, lo, gap);
+    const long long line0 = sh.begin(my_w);
+    // the row of tile line0: the lane whose rows hold it, then (long batches) the row among them
+    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, line0 < (before + mine) * U)) - 1;
+    long long row0 = __shfl_sync(0xFFFFFFFFu, before, src) * U;
+    int cr = src * per;
+    if (per == 1) {
+      len = __shfl_sync(0xFFFFFFFFu, len, src);
+    } else {
+      for (; cr < p.R; cr += 32) {
+        const int l = cr + lane < p.R ? row_len(cr + lane) : -1;
+        const long long t = row_tiles(l), a = warp_scan(t, lane);
+        const unsigned b = __ballot_sync(0xFFFFFFFFu, line0 < row0 + a * U);
+        if (b) {
+          const int x = __ffs(b) - 1;
+          cr += x;
+          len = __shfl_sync(0xFFFFFFFFu, l, x);
+          row0 += __shfl_sync(0xFFFFFFFFu, a - t, x) * U;
+          break;
+        }
+        row0 += __shfl_sync(0xFFFFFFFFu, a, 31) * U;
+      }
+    }
+    int lo, gap, n_vis = visible(len, lo, gap);
     int tiles = row_tiles(len);
-    int cu = (int)(start_in[warp] / tiles), ct = (int)(start_in[warp] - (long long)cu * tiles);
+    int cu = (int)quotient(line0 - row0, tiles), ct = (int)(line0 - row0 - (long long)cu * tiles);
+    const int ct0 = ct;
+    // ---- cursor: the next tile to look up
     int todo = count;  // tiles not yet looked up
     bool first = true;
-    const long long line0 = sh.begin(my_w);
     const int tok_lane = lane & (Z::TT - 1);
 
     int nx_page = -1, nx_off = 0, nx_r = 0, nx_u = 0, nx_flags = 0;
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
       if (nx_want) {
         int j, tok;
         if (p.sel) {
-          const int e = div_page(x);
+          const int e = p.by_page(x);
           j = __ldg(p.sel + ((long long)cr * p.Hkv + cu / p.n_chunks) * p.topk + e);
           nx_off = x - e * p.page;
           if (j < 0 || j >= p.W) {
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
           }
         } else {
           tok = x < lo ? x : x + gap;
-          j = div_page(tok);
+          j = p.by_page(tok);
           nx_off = tok - j * p.page;
         }
         if (nx_want) nx_page = __ldg(p.table + cr * p.table_stride + j);
@@ -394,6 +399,56 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
     uint32_t qf[NT][D / 16][2];
     float cs[NT][2];  // log2 score per product, for heads 2 t4 and 2 t4 + 1 of each 8
     float m[NT][2], l[NT][2], acc[NT][D / 16][4];
+    auto load_q = [&](int r, int h, int hc0, int n_heads) {
+      const T* q = reinterpret_cast<const T*>(p.q) + r * p.q_sb + (long long)(h * p.G + hc0) * p.q_sh;
+      const float c0 = p.scale_log2 * (F8 && p.ks ? __ldg(p.ks + h) : 1.f);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int hd = nt * 8 + g8;
+        const bool in = hd < n_heads;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          // an 8-bit row's fragment has channels 16 c + 4 t4 ..+3, a 16-bit row's 16 c + 2 t4, +1, +8, +9
+          const int d0 = 16 * c + (F8 ? 4 * t4 : 2 * t4), d1 = d0 + (F8 ? 2 : 8);
+          qf[nt][c][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d0)) : 0u;
+          qf[nt][c][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d1)) : 0u;
+        }
+        float inv = 1.f;
+        if constexpr (F8 && std::is_same<T, __nv_bfloat16>::value) {
+          float big = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 x = unpack2<T>(qf[nt][c][e]);
+              big = fmaxf(big, fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+          big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+          // big 2^f in [2^14, 2^15); |f| <= 126 so that both powers are normal numbers
+          const int ex = (int)(__float_as_uint(big) >> 23);
+          const int f = ex == 255 ? 0 : max(-113, min(126, 141 - ex));
+          const float mul = __uint_as_float((uint32_t)(127 + f) << 23);
+          inv = __uint_as_float((uint32_t)(127 - f) << 23);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 x = unpack2<T>(qf[nt][c][e]);
+              qf[nt][c][e] = pack2<__half>(x.x * mul, x.y * mul);
+            }
+        }
+        const float ch = c0 * inv;
+        cs[nt][0] = __shfl_sync(0xFFFFFFFFu, ch, 8 * t4);
+        cs[nt][1] = __shfl_sync(0xFFFFFFFFu, ch, 8 * t4 + 4);
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][c][e] = 0.f;
+      }
+    };
     int piece_t0 = 0, piece_n = 0;
     bool unit_begin = false;
     int stage = 0;
@@ -402,6 +457,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
     const int v_row = (lane & 7) + (lane >> 4) * 8, v_pc = (lane >> 3) & 1;
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
+      __syncwarp();
+      const int2 mt = meta[warp][stage];
+      const unsigned mask = (unsigned)mt.x;
+      const int r = mt.y >> 16, u = mt.y >> 4 & 4095, flags = mt.y & 15;
+      const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC;  // key head, first query head of the chunk
+      const int n_heads = min(Z::HC, p.G - hc0);
+      if (flags & 1) load_q(r, h, hc0, n_heads);
       cp_async_wait<Z::S - 2>();
       __syncwarp();
       if (i + Z::S - 1 < count) {
@@ -409,60 +471,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
         if (todo > 0) lookup();
       }
       cp_async_commit();
-      const int2 mt = meta[warp][stage];
-      const unsigned mask = (unsigned)mt.x;
-      const int r = mt.y >> 16, u = mt.y >> 4 & 4095, flags = mt.y & 15;
-      const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC;  // key head, first query head of the chunk
-      const int n_heads = min(Z::HC, p.G - hc0);
       if (flags & 1) {
-        const T* q = reinterpret_cast<const T*>(p.q) + r * p.q_sb + (long long)(h * p.G + hc0) * p.q_sh;
-        const float c0 = p.scale_log2 * (F8 && p.ks ? __ldg(p.ks + h) : 1.f);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int hd = nt * 8 + g8;
-          const bool in = hd < n_heads;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            // an 8-bit row's fragment has channels 16 c + 4 t4 ..+3, a 16-bit row's 16 c + 2 t4, +1, +8, +9
-            const int d0 = 16 * c + (F8 ? 4 * t4 : 2 * t4), d1 = d0 + (F8 ? 2 : 8);
-            qf[nt][c][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d0)) : 0u;
-            qf[nt][c][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d1)) : 0u;
-          }
-          float inv = 1.f;
-          if constexpr (F8 && std::is_same<T, __nv_bfloat16>::value) {
-            float big = 0.f;
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float2 x = unpack2<T>(qf[nt][c][e]);
-                big = fmaxf(big, fmaxf(fabsf(x.x), fabsf(x.y)));
-              }
-            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-            // big 2^f in [2^14, 2^15); |f| <= 126 so that both powers are normal numbers
-            const int ex = (int)(__float_as_uint(big) >> 23);
-            const int f = ex == 255 ? 0 : max(-113, min(126, 141 - ex));
-            const float mul = __uint_as_float((uint32_t)(127 + f) << 23);
-            inv = __uint_as_float((uint32_t)(127 - f) << 23);
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float2 x = unpack2<T>(qf[nt][c][e]);
-                qf[nt][c][e] = pack2<__half>(x.x * mul, x.y * mul);
-              }
-          }
-          const float ch = c0 * inv;
-          cs[nt][0] = __shfl_sync(0xFFFFFFFFu, ch, 8 * t4);
-          cs[nt][1] = __shfl_sync(0xFFFFFFFFu, ch, 8 * t4 + 4);
-          m[nt][0] = m[nt][1] = -INFINITY;
-          l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][c][e] = 0.f;
-        }
         piece_n = 0;
         piece_t0 = i;
         unit_begin = (flags & 4) != 0;
@@ -646,9 +655,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
             }
           }
           if (lane == 0) {
-            // the piece's first tile within its unit: known from the share's start, or 0
             const int tl = row_tiles(row_len(r));
-            const int tb = is_first ? (int)(start_in[warp] % tl) : 0;
+            const int tb = is_first ? ct0 : 0;
             Part& pt = parts[slot];
             pt.r = r;
             pt.u = u;
@@ -670,38 +678,43 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
     return reinterpret_cast<const float*>((i & 1) ? smem + (i >> 1) * Z::WARP : smem + kWarps * Z::WARP + (i >> 1) * Z::PART);
   };
   const int hcw = min(Z::HC, p.G);  // heads of a workspace part
+  // lane j holds part j (2 w: warp w's first, 2 w + 1: its last); parts of one unit are neighbours
+  const int my_part = lane & (2 * kWarps - 1);
+  const Part mp = parts[my_part];
+  unsigned todo = __ballot_sync(0xFFFFFFFFu, lane < 2 * kWarps && mp.te > 0);
 #pragma unroll 1
-  for (int i = 0; i < 2 * kWarps;) {
-    if (parts[i].te == 0) {
-      ++i;
-      continue;
-    }
-    const Part a = parts[i];
-    int end = i + 1, te = a.te;
-    for (int j = i + 1; j < 2 * kWarps; ++j) {
-      if (parts[j].te == 0) continue;
-      if (parts[j].r != a.r || parts[j].u != a.u) break;
-      end = j + 1;
-      te = parts[j].te;
-    }
-    const int h = a.u / p.n_chunks, hc0 = (a.u - h * p.n_chunks) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
-    const bool whole = a.tb == 0 && te == a.tiles;
+  while (todo) {
+    const int i = __ffs(todo) - 1;
+    const int r = __shfl_sync(0xFFFFFFFFu, mp.r, i), u = __shfl_sync(0xFFFFFFFFu, mp.u, i);
+    const unsigned grp = __ballot_sync(0xFFFFFFFFu, mp.r == r && mp.u == u) & todo;
+    todo &= ~grp;
+    const int tb = __shfl_sync(0xFFFFFFFFu, mp.tb, i), tiles = __shfl_sync(0xFFFFFFFFu, mp.tiles, i);
+    const int te = __shfl_sync(0xFFFFFFFFu, mp.te, 31 - __clz(grp));
+    const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
+    const bool whole = tb == 0 && te == tiles;
     const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
-    T* o = reinterpret_cast<T*>(p.o) + a.r * p.o_sb + (long long)(h * p.G + hc0) * p.o_sh;
-    float* lse = p.lse + (size_t)a.r * p.H + h * p.G + hc0;
-    const size_t ws = (size_t)(2 * blockIdx.x + (a.tb == 0 ? 1 : 0)) * hcw;
+    T* o = reinterpret_cast<T*>(p.o) + r * p.o_sb + (long long)(h * p.G + hc0) * p.o_sh;
+    float* lse = p.lse + (size_t)r * p.H + h * p.G + hc0;
+    const size_t ws = (size_t)(2 * blockIdx.x + (tb == 0 ? 1 : 0)) * hcw;
     for (int hd = warp; hd < n_heads; hd += kWarps) {
-      float top = -INFINITY, sum = 0.f;
-      for (int j = i; j < end; ++j)
-        if (parts[j].te) top = fmaxf(top, part_o(j)[hd * Z::LD + D]);
+      const float* ml = part_o(my_part) + hd * Z::LD + D;
+      const bool in = grp >> lane & 1u;
+      float top = in ? ml[0] : -INFINITY;
+      const float m = top, l = in ? ml[1] : 0.f;
+#pragma unroll
+      for (int q = 2 * kWarps / 2; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, q));
+      top = __shfl_sync(0xFFFFFFFFu, top, 0);
       const float base = top == -INFINITY ? 0.f : top;
+      const float wl = exp2f(m - base);
+      float sum = wl * l;
+#pragma unroll
+      for (int q = 2 * kWarps / 2; q > 0; q >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, q);
+      sum = __shfl_sync(0xFFFFFFFFu, sum, 0);
       V4 x;
       std::memset(&x, 0, sizeof(x));
-      for (int j = i; j < end; ++j) {
-        if (!parts[j].te) continue;
-        const float w = exp2f(part_o(j)[hd * Z::LD + D] - base);
-        sum = fmaf(w, part_o(j)[hd * Z::LD + D + 1], sum);
-        axpy(x, w, *reinterpret_cast<const V4*>(part_o(j) + hd * Z::LD + lane * VL));
+      for (unsigned b = grp; b; b &= b - 1) {
+        const int j = __ffs(b) - 1;
+        axpy(x, __shfl_sync(0xFFFFFFFFu, wl, j), *reinterpret_cast<const V4*>(part_o(j) + hd * Z::LD + lane * VL));
       }
       if (whole) {
         store_out(o + hd * p.o_sh + lane * VL, x, sum == 0.f ? 0.f : vs / sum);
@@ -711,50 +724,57 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
         if (lane == 0) *reinterpret_cast<float2*>(p.ws_ml + (ws + hd) * 2) = make_float2(top, sum);
       }
     }
-    if (!whole) {
-      const int b0 = sh.warp_of(a.unit0) / kWarps, b1 = sh.warp_of(a.unit0 + a.tiles - 1) / kWarps;
+    if (whole) continue;
+    const long long unit0 = __shfl_sync(0xFFFFFFFFu, mp.unit0, i);
+    const int b0 = sh.warp_of(unit0) / kWarps, n = sh.warp_of(unit0 + tiles - 1) / kWarps - b0 + 1;
+    __syncthreads();  // the block's part is written; the fence passes that on
+    if (tid == 0) {
       __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomicAdd(p.counters + b0, 1) == b1 - b0;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        if (tid == 0) p.counters[b0] = 0;
-        const int n = b1 - b0 + 1;
-        for (int hd = warp; hd < n_heads; hd += kWarps) {
-          auto ml = [&](int j) {
-            return __ldcg(reinterpret_cast<const float2*>(p.ws_ml + ((size_t)(2 * (b0 + j) + (j == 0 ? 1 : 0)) * hcw + hd) * 2));
-          };
-          float top = -INFINITY;
-          for (int j = lane; j < n; j += 32) top = fmaxf(top, ml(j).x);
+      s_last = atomicAdd(p.counters + b0, 1) == n - 1;
+      __threadfence();
+    }
+    __syncthreads();
+    if (s_last) {
+      if (tid == 0) p.counters[b0] = 0;
+      for (int hd = warp; hd < n_heads; hd += kWarps) {
+        auto at = [&](int j) { return (size_t)(2 * (b0 + j) + (j == 0 ? 1 : 0)) * hcw + hd; };
+        auto ml = [&](int j) {
+          return j < n ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml + at(j) * 2)) : make_float2(-INFINITY, 0.f);
+        };
+        const float2 ml0 = ml(lane);
+        float top = ml0.x;
+        for (int j = 32 + lane; j < n; j += 32) top = fmaxf(top, ml(j).x);
 #pragma unroll
-          for (int q = 16; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, q));
-          const float base = top == -INFINITY ? 0.f : top;
-          V4 x;
-          std::memset(&x, 0, sizeof(x));
-          float sum = 0.f;
-          for (int j0 = 0; j0 < n; j0 += 32) {
-            const float2 v = j0 + lane < n ? ml(j0 + lane) : make_float2(-INFINITY, 0.f);
-            const float wl = exp2f(v.x - base);
-            sum = fmaf(wl, v.y, sum);
-            const int jn = min(32, n - j0);
-#pragma unroll 8
-            for (int j = 0; j < jn; ++j) {
-              const float w = __shfl_sync(0xFFFFFFFFu, wl, j);
-              const int b = b0 + j0 + j;
-              axpy(x, w, __ldcg(reinterpret_cast<const V4*>(
-                             p.ws_o + ((size_t)(2 * b + (b == b0 ? 1 : 0)) * hcw + hd) * D + lane * VL)));
+        for (int q = 16; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, q));
+        const float base = top == -INFINITY ? 0.f : top;
+        V4 x;
+        std::memset(&x, 0, sizeof(x));
+        float sum = 0.f;
+        for (int j0 = 0; j0 < n; j0 += 32) {
+          const float2 v = j0 == 0 ? ml0 : ml(j0 + lane);
+          const float wl = exp2f(v.x - base);
+          sum = fmaf(wl, v.y, sum);
+          constexpr int kBatch = 16;  // loads in flight
+#pragma unroll 1
+          for (int jb = 0; jb < min(32, n - j0); jb += kBatch) {
+            V4 y[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+              if (j0 + jb + e < n) y[e] = __ldcg(reinterpret_cast<const V4*>(p.ws_o + at(j0 + jb + e) * D + lane * VL));
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+              const float w = __shfl_sync(0xFFFFFFFFu, wl, jb + e);
+              if (j0 + jb + e < n) axpy(x, w, y[e]);
             }
           }
-#pragma unroll
-          for (int q = 16; q > 0; q >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, q);
-          store_out(o + hd * p.o_sh + lane * VL, x, sum == 0.f ? 0.f : vs / sum);
-          if (lane == 0) lse[hd] = sum == 0.f ? -INFINITY : (base - kShift + log2f(sum)) * 0.69314718055994531f;
         }
+#pragma unroll
+        for (int q = 16; q > 0; q >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, q);
+        store_out(o + hd * p.o_sh + lane * VL, x, sum == 0.f ? 0.f : vs / sum);
+        if (lane == 0) lse[hd] = sum == 0.f ? -INFINITY : (base - kShift + log2f(sum)) * 0.69314718055994531f;
       }
-      __syncthreads();  // s_last has been read
     }
-    i = end;
+    __syncthreads();  // s_last has been read
   }
 }
 
@@ -762,25 +782,29 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
 // host
 // ---------------------------------------------------------------------------------------
 template <int D, typename T, bool F8, int NT>
-cudaError_t launch(const PageAttnParams& p, int blocks, cudaStream_t st) {
+cudaError_t launch(const PageAttnParams& p, int blocks, int dev, cudaStream_t st) {
   using Z = Shape<D, F8, NT>;
   auto fn = page_attn_kernel<D, T, F8, NT>;
-  const cudaError_t rc = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
-  if (rc != cudaSuccess) return rc;
+  static std::atomic<uint64_t> ready{0};  // devices (by bit) on which the limit is raised
+  if (!(ready.load(std::memory_order_acquire) >> dev & 1u)) {
+    const cudaError_t rc = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
+    if (rc != cudaSuccess) return rc;
+    ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
   fn<<<(unsigned)blocks, kThreads, Z::SMEM, st>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, typename T, bool F8>
-cudaError_t launch_nt(const PageAttnParams& p, int blocks, cudaStream_t st) {
-  return p.G <= 8 ? launch<D, T, F8, 1>(p, blocks, st) : launch<D, T, F8, 2>(p, blocks, st);
+cudaError_t launch_nt(const PageAttnParams& p, int blocks, int dev, cudaStream_t st) {
+  return p.G <= 8 ? launch<D, T, F8, 1>(p, blocks, dev, st) : launch<D, T, F8, 2>(p, blocks, dev, st);
 }
 
 template <int D>
-cudaError_t launch_d(const PageAttnParams& p, int q_dtype, int kv_dtype, int blocks, cudaStream_t st) {
+cudaError_t launch_d(const PageAttnParams& p, int q_dtype, int kv_dtype, int blocks, int dev, cudaStream_t st) {
   if (kv_dtype == VKV_E4M3)
-    return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, true>(p, blocks, st) : launch_nt<D, __half, true>(p, blocks, st);
-  return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, false>(p, blocks, st) : launch_nt<D, __half, false>(p, blocks, st);
+    return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, true>(p, blocks, dev, st) : launch_nt<D, __half, true>(p, blocks, dev, st);
+  return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, false>(p, blocks, dev, st) : launch_nt<D, __half, false>(p, blocks, dev, st);
 }
 
 // Bytes of the counters and of one block's two workspace parts.
@@ -820,7 +844,8 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   if (!page_tensor_aligned(q, a->q_dtype) || !page_tensor_aligned(o, a->q_dtype) ||
       !page_tensor_aligned(a->k, a->kv_dtype) || !page_tensor_aligned(a->v, a->kv_dtype))
     return VKV_ERR_ALIGN;
-  const int n_sm = device_sm_count(nullptr);
+  int dev = 0;
+  const int n_sm = device_sm_count(&dev);
   if (n_sm <= 0) return VKV_ERR_CUDA;
   const size_t need = vkv_page_attn_workspace_size(a->H, a->Hkv, a->d);
   if (!a->workspace || a->workspace_bytes < need) return VKV_ERR_WORKSPACE;
@@ -829,8 +854,7 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   std::memset(&p, 0, sizeof(p));
   p.R = a->R; p.H = a->H; p.Hkv = a->Hkv; p.G = a->H / a->Hkv;
   p.page = a->page; p.n_pages = a->n_pages; p.W = a->W; p.sink = a->sink; p.window = a->window; p.topk = a->topk;
-  while ((1ll << p.div_shift) < a->page) ++p.div_shift;
-  p.div_mul = (uint32_t)((((1ull << p.div_shift) - (uint32_t)a->page) << 32) / (uint32_t)a->page + 1);
+  p.by_page = fast_div(a->page);
   const int hc = p.G <= 8 ? 8 : 16;
   p.n_chunks = (p.G + hc - 1) / hc;
   p.scale_log2 = a->scale * 1.4426950408889634f;
@@ -859,7 +883,7 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   const long long tiles = ((most + tt - 1) / tt) * a->R * a->Hkv * p.n_chunks;
   const int blocks = (int)std::min<long long>(all, (tiles + kMinTiles * kWarps - 1) / (kMinTiles * kWarps));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t rc = a->d == 128 ? launch_d<128>(p, a->q_dtype, a->kv_dtype, blocks, st)
-                                     : launch_d<64>(p, a->q_dtype, a->kv_dtype, blocks, st);
+  const cudaError_t rc = a->d == 128 ? launch_d<128>(p, a->q_dtype, a->kv_dtype, blocks, dev, st)
+                                     : launch_d<64>(p, a->q_dtype, a->kv_dtype, blocks, dev, st);
   return rc == cudaSuccess ? VKV_OK : VKV_ERR_CUDA;
 }

@@ -1,30 +1,31 @@
 // vkv_page_map: pages and slots of one step's new tokens, from the rows' lengths.
 //
-// One thread-block cluster does the step.  Every CTA reads all rows (a few KB, from
-// L2 after the first) and scans them for itself: tokens, pages taken and pages returned
-// before each row.  So no CTA waits for another's result, and the tokens, the new table
-// entries and the returned pages can be spread over the cluster's threads, each of which
-// finds its row by bisection of the scan in shared memory.  The lengths and ring
-// positions may be updated in place: they are written only after a cluster barrier
-// behind every CTA's reads.
+// Every block reads all rows (a few KB, from L2 after the first) and scans them for itself:
+// tokens, pages taken and pages returned before each row.  So no block waits for another's
+// result, and the tokens, the new table entries and the returned pages can be spread over
+// the grid's threads, each of which finds its row by bisection of the scan in shared memory.
+// Where lengths or ring positions are updated in place, they may be written only after every
+// block has read them: those steps run as one cluster, with a cluster barrier in between.
 //
 // Bound: latency.  A decoding step moves some tens of KB; its time is the launch, two
-// dependent reads (lengths, then ring or table) and the stores.
+// dependent reads (lengths, then ring or table) and the stores.  A thread takes kTok tokens
+// at a time, so that their bisections and look-ups overlap.
 #include <algorithm>
 #include <climits>
 #include <cstring>
 
-#include "vkv_internal.h"
-#include "vkv_ptx.cuh"
+#include "vkv_page.cuh"
 
 namespace vkv {
 namespace {
 
 constexpr int kMapThreads = 512;
 constexpr int kMapMaxCluster = 8;
+constexpr int kTok = 4;
 
 struct MapParams {
   int R, W, page, n_ring, max_tokens;
+  FastDiv by_page;
   const int* kv_len;
   const int* new_len;
   int* table;
@@ -40,16 +41,6 @@ struct MapParams {
   int* err;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
 // All threads of the cluster; memory operations before it are visible after it.
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -71,6 +62,7 @@ __device__ __forceinline__ unsigned ring_at(int first, int i, int n) {
   return x >= (unsigned)n ? x - (unsigned)n : x;
 }
 
+template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p) {
   extern __shared__ int sm[];
   int* tok = sm;               // [R + 1] new tokens before row r
@@ -165,9 +157,9 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
       back[R] = (int)n_back;
     }
   }
-  cluster_barrier();  // every CTA has read the lengths and positions; the scan is in shared memory
-  const int rank = (int)cluster_rank();
-  const int n_thr = (int)cluster_size() * kMapThreads, me = rank * kMapThreads + tid;
+  if constexpr (IN_PLACE) cluster_barrier();  // the grid is one cluster: every block has read what is updated
+  else __syncthreads();
+  const int n_thr = (int)gridDim.x * kMapThreads, me = (int)blockIdx.x * kMapThreads + tid;
   const int total = bad ? 0 : (int)all_t;
   if (me == 0) {
     if (bad && p.err) atomicCAS(p.err, 0, bad);
@@ -193,7 +185,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   if (!bad) {
     for (int i = me; i < (int)n_need; i += n_thr) {  // new table entries
       const int r = find_row(need, R, i);
-      const int had = (int)(((long long)held[r] + page - 1) / page);
+      const int had = p.by_page(held[r]) + (p.by_page(held[r]) * page < held[r] ? 1 : 0);
       p.table[r * p.table_stride + had + (i - need[r])] = p.ring[ring_at(ring_t, i, p.n_ring)];
     }
     const int ring_b = (int)(returned % p.n_ring);
@@ -202,25 +194,37 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
       p.ring[ring_at(ring_b, i, p.n_ring)] = p.table[r * p.table_stride + (i - back[r])];
     }
   }
-  for (int i = me; i < p.max_tokens; i += n_thr) {
-    long long s = -1;
-    int r = -1, t = -1;
-    if (i < total) {
-      r = find_row(tok, R, i);
-      t = held[r] + (i - tok[r]);
-      const int j = t / page, had = (int)(((long long)held[r] + page - 1) / page);
-      int pg;
-      if (j < had) {
-        pg = p.table[r * p.table_stride + j];
-      } else {
-        pg = p.ring[ring_at(ring_t, need[r] + (j - had), p.n_ring)];
-      }
-      s = (long long)pg * page + (t - j * page);
-      if (s < 0) s = -1;
+  for (long long i0 = me; i0 < p.max_tokens; i0 += (long long)kTok * n_thr) {
+    int row[kTok], t[kTok], pg[kTok];
+#pragma unroll
+    for (int e = 0; e < kTok; ++e) row[e] = 0;
+    for (int n = R; n > 1;) {  // largest row with tok[row] <= i
+      const int half = n >> 1;
+#pragma unroll
+      for (int e = 0; e < kTok; ++e)
+        if (tok[row[e] + half] <= i0 + (long long)e * n_thr) row[e] += half;
+      n -= half;
     }
-    p.slot[i] = s;
-    if (p.row) p.row[i] = r;
-    if (p.pos) p.pos[i] = t;
+#pragma unroll
+    for (int e = 0; e < kTok; ++e) {
+      const long long i = i0 + (long long)e * n_thr;
+      pg[e] = -1;
+      if (i >= total) continue;
+      const int r = row[e], h = held[r];
+      t[e] = h + (int)(i - tok[r]);
+      const int j = p.by_page(t[e]), had = p.by_page(h) + (p.by_page(h) * page < h ? 1 : 0);
+      pg[e] = j < had ? p.table[r * p.table_stride + j]
+                      : p.ring[ring_at(ring_t, need[r] + (j - had), p.n_ring)];
+    }
+#pragma unroll
+    for (int e = 0; e < kTok; ++e) {
+      const long long i = i0 + (long long)e * n_thr;
+      if (i >= p.max_tokens) break;
+      const bool in = i < total;
+      p.slot[i] = in && pg[e] >= 0 ? (long long)pg[e] * page + (t[e] - p.by_page(t[e]) * page) : -1;
+      if (p.row) p.row[i] = in ? row[e] : -1;
+      if (p.pos) p.pos[i] = in ? t[e] : -1;
+    }
   }
 }
 
@@ -238,8 +242,8 @@ extern "C" vkv_status vkv_page_map(const vkv_page_map_args* a, vkv_stream_t stre
   if (!a->kv_len || !a->new_len || !a->table || !a->ring || !a->ring_pos || !a->kv_len_out || !a->ring_pos_out ||
       !a->slot)
     return VKV_ERR_NULL;
-  int dev = 0;
-  if (device_sm_count(&dev) <= 0) return VKV_ERR_CUDA;
+  const int n_sm = device_sm_count(nullptr);
+  if (n_sm <= 0) return VKV_ERR_CUDA;
   MapParams p;
   std::memset(&p, 0, sizeof(p));
   p.R = a->R;
@@ -260,10 +264,14 @@ extern "C" vkv_status vkv_page_map(const vkv_page_map_args* a, vkv_stream_t stre
   p.pos = a->pos;
   p.cu = a->cu;
   p.err = a->err_word;
-  const int ctas = (int)std::min<long long>(kMapMaxCluster, ((long long)std::max(a->max_tokens, a->R) + kMapThreads - 1) / kMapThreads);
+  p.by_page = fast_div(a->page);
+  const bool in_place = a->kv_len == a->kv_len_out || a->ring_pos == a->ring_pos_out;
+  const int most = in_place ? kMapMaxCluster : n_sm;
+  const int ctas = (int)std::min<long long>(most, ((long long)std::max(a->max_tokens, a->R) + kMapThreads - 1) / kMapThreads);
   const size_t smem = (size_t)(4 * a->R + 3) * sizeof(int);
+  auto fn = in_place ? page_map_kernel<true> : page_map_kernel<false>;
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return VKV_ERR_CUDA;
   }
@@ -278,8 +286,8 @@ extern "C" vkv_status vkv_page_map(const vkv_page_map_args* a, vkv_stream_t stre
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, page_map_kernel, p) != cudaSuccess) {
+  cfg.numAttrs = in_place ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
     cudaGetLastError();
     return VKV_ERR_CUDA;
   }

@@ -766,55 +766,77 @@ _page_attn_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, clear
 _page_select_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, grown on demand
 
 
-def _on(device, stream, *tensors):
-    """The stream handle for a call on `device`, after checking that every tensor lives there."""
-    for x in tensors:
-        if x is not None and x.device != device:
-            raise ValueError(f"tensors on different devices: {x.device} and {device}")
-    if device.type != "cuda":
-        raise ValueError("expected CUDA tensors")
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+
+
+def _handle(di, stream):
+    """The stream handle for a call on device `di`."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(di)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _call_page(name, fmt, device, sh, *values):
-    """One C call under `device`; raises VkvError on a non-OK status."""
+def _call_page(name, fmt, di, sh, *values):
+    """One C call with device `di` current; raises VkvError on a non-OK status."""
     fn = getattr(_lib or lib(), name)
-    if device.index == torch._C._cuda_getDevice():
+    if di == torch._C._cuda_getDevice():
         status = fn(fmt.pack(*values), sh)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(di):
             status = fn(fmt.pack(*values), sh)
     if status:
         _check(status, name)
 
 
-def _ints(x, what, dtype, *shape):
-    """`x`, checked to be a contiguous `dtype` tensor of `shape` (None entries are free)."""
-    if x.dtype != dtype or not x.is_contiguous() or x.dim() != len(shape) or any(
-            want is not None and have != want for have, want in zip(x.shape, shape)):
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape}, got {x.dtype} {tuple(x.shape)}")
-    return x
+def _place(x):
+    di = x.get_device()
+    if di < 0:
+        raise ValueError("expected CUDA tensors")
+    return di
 
 
-def _ptr(x):
-    return 0 if x is None else x.data_ptr()
+def _vec(x, what, dtype, shape, di):
+    """The address of `x`, checked to be a contiguous `dtype` tensor of `shape` on device `di`."""
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != di or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on cuda:{di}, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
 
 
-def _page_table(table, R):
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != R or (
-            table.shape[1] > 1 and table.stride(1) != 1):
+def _opt(x, what, dtype, shape, di):
+    return 0 if x is None else _vec(x, what, dtype, shape, di)
+
+
+def _err(err, di):
+    if err is None:
+        return 0
+    if err.dtype is not _I32 or err.get_device() != di or err.numel() < 1:
+        raise ValueError(f"err must be an int32 tensor on cuda:{di}")
+    return err.data_ptr()
+
+
+def _page_table(table, R, di):
+    """(address, row stride, columns) of a block table."""
+    if table.dtype is not _I32 or table.ndim != 2 or table.get_device() != di:
+        raise ValueError(f"block_table must be an int32 tensor [R, W] on cuda:{di}")
+    rows, W = table.shape
+    stride, inner = table.stride()
+    if rows != R or (W > 1 and inner != 1):
         raise ValueError("block_table must be an int32 tensor [R, W] with contiguous rows")
     # a single row's stride is never used; a narrower one than W means overlapping rows
-    return max(table.stride(0), table.shape[1]) if R == 1 else table.stride(0)
+    return table.data_ptr(), max(stride, W) if R == 1 else stride, W
 
 
-def _cache(k, v):
-    """(pages, tokens per page, key heads, d, dtype code) of a paged cache pair."""
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride(3) != 1 or v.stride(3) != 1:
-        raise ValueError("k_pages and v_pages must be [n_pages, page, Hkv, d] of one type with contiguous d")
-    return (*k.shape, _dtype(k, "the cache"))
+def _cache(k, v, di):
+    """(pages, tokens per page, key heads, d, dtype code, k's and v's vkv_tensor fields) of a paged cache pair."""
+    N, P, Hkv, d = shape = k.shape
+    if shape != v.shape or k.dtype is not v.dtype or k.get_device() != di or v.get_device() != di:
+        raise ValueError(f"k_pages and v_pages must be [n_pages, page, Hkv, d] of one type on cuda:{di}")
+    k0, k1, k2, k3 = k.stride()
+    v0, v1, v2, v3 = v.stride()
+    if k3 != 1 or v3 != 1:
+        raise ValueError("k_pages and v_pages must have a contiguous last axis")
+    return N, P, Hkv, d, _dtype(k, "the cache"), (k.data_ptr(), k0, k1, k2, v.data_ptr(), v0, v1, v2)
 
 
 def _dtype(x, what):
@@ -824,14 +846,12 @@ def _dtype(x, what):
         raise ValueError(f"{what}: {x.dtype} is not one of bfloat16, float16, float8_e4m3fn") from None
 
 
-def _scales(k_scale, v_scale, kv_dtype, Hkv):
+def _scales(k_scale, v_scale, kv_dtype, Hkv, di):
     if k_scale is None and v_scale is None:
-        return
+        return 0, 0
     if kv_dtype != DTYPE_E4M3:
         raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache")
-    for x, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if x is not None:
-            _ints(x, what, torch.float32, Hkv)
+    return _opt(k_scale, "k_scale", _F32, (Hkv,), di), _opt(v_scale, "v_scale", _F32, (Hkv,), di)
 
 
 def page_map(kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens, out=None, err=None, stream=None):
@@ -841,35 +861,28 @@ def page_map(kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens
     ends).  block_table int32 [R, W] and ring int32 [n] (free page numbers, ring[t % n] for
     ring_pos[0] <= t < ring_pos[1]) are updated in place; ring_pos int64 [2].
     Returns (or fills `out`) dict(kv_len, ring [the new ring_pos], slot int64 [max_tokens],
-    row, pos int32 [max_tokens], cu int32 [R + 1]); out["kv_len"] may be kv_len itself and
-    out["ring"] ring_pos.  A step that does not fit changes nothing and sets err.
+    row, pos int32 [max_tokens], cu int32 [R + 1]; of a given `out` the last three may be
+    missing); out["kv_len"] may be kv_len itself and out["ring"] ring_pos.  A step that does
+    not fit changes nothing and sets err.
     """
-    R, dev = kv_len.shape[0], kv_len.device
+    R, di = kv_len.shape[0], _place(kv_len)
     max_tokens = int(max_tokens)
     if out is None:
-        i32 = dict(dtype=torch.int32, device=dev)
-        out = {"kv_len": torch.empty(R, **i32), "ring": torch.empty(2, dtype=torch.int64, device=dev),
-               "slot": torch.empty(max_tokens, dtype=torch.int64, device=dev),
-               "row": torch.empty(max_tokens, **i32), "pos": torch.empty(max_tokens, **i32),
-               "cu": torch.empty(R + 1, **i32)}
-    row, pos, cu = out.get("row"), out.get("pos"), out.get("cu")
-    sh = _on(dev, stream, new_len, block_table, ring, ring_pos, out["kv_len"], out["ring"], out["slot"], row, pos, cu,
-             err)
-    _ints(kv_len, "kv_len", torch.int32, R)
-    _ints(new_len, "new_len", torch.int32, R)
-    _ints(ring, "ring", torch.int32, None)
-    _ints(ring_pos, "ring_pos", torch.int64, 2)
-    _ints(out["kv_len"], "out['kv_len']", torch.int32, R)
-    _ints(out["ring"], "out['ring']", torch.int64, 2)
-    _ints(out["slot"], "out['slot']", torch.int64, max_tokens)
-    for x, what, n in ((row, "row", max_tokens), (pos, "pos", max_tokens), (cu, "cu", R + 1)):
-        if x is not None:
-            _ints(x, f"out['{what}']", torch.int32, n)
-    stride = _page_table(block_table, R)
-    _call_page("vkv_page_map", _PAGE_MAP, dev, sh, R, block_table.shape[1], int(page_size), ring.shape[0], max_tokens, 0,
-               kv_len.data_ptr(), new_len.data_ptr(), block_table.data_ptr(), stride, ring.data_ptr(),
-               ring_pos.data_ptr(), out["kv_len"].data_ptr(), out["ring"].data_ptr(), out["slot"].data_ptr(),
-               _ptr(row), _ptr(pos), _ptr(cu), _ptr(err))
+        dev = kv_len.device
+        out = {"kv_len": torch.empty(R, dtype=_I32, device=dev), "ring": torch.empty(2, dtype=_I64, device=dev),
+               "slot": torch.empty(max_tokens, dtype=_I64, device=dev),
+               "row": torch.empty(max_tokens, dtype=_I32, device=dev),
+               "pos": torch.empty(max_tokens, dtype=_I32, device=dev), "cu": torch.empty(R + 1, dtype=_I32, device=dev)}
+    table, stride, W = _page_table(block_table, R, di)
+    rows, tokens, n_ring = (R,), (max_tokens,), ring.shape[0]
+    get = out.get
+    _call_page("vkv_page_map", _PAGE_MAP, di, _handle(di, stream), R, W, int(page_size), n_ring, max_tokens, 0,
+               _vec(kv_len, "kv_len", _I32, rows, di), _vec(new_len, "new_len", _I32, rows, di), table, stride,
+               _vec(ring, "ring", _I32, (n_ring,), di), _vec(ring_pos, "ring_pos", _I64, (2,), di),
+               _vec(out["kv_len"], "out['kv_len']", _I32, rows, di), _vec(out["ring"], "out['ring']", _I64, (2,), di),
+               _vec(out["slot"], "out['slot']", _I64, tokens, di), _opt(get("row"), "out['row']", _I32, tokens, di),
+               _opt(get("pos"), "out['pos']", _I32, tokens, di), _opt(get("cu"), "out['cu']", _I32, (R + 1,), di),
+               _err(err, di))
     return out
 
 
@@ -880,40 +893,54 @@ def page_append(k_new, v_new, slot, k_pages, v_pages, k_scale=None, v_scale=None
     x / scale, fp32 scales [Hkv]); kbar (optional fp32 [n_pages, Hkv, d]) receives the key
     mean of each page written to.
     """
-    N, P, Hkv, d, kv_dtype = _cache(k_pages, v_pages)
-    T, dev = k_new.shape[0], k_pages.device
-    if k_new.shape != (T, Hkv, d) or v_new.shape != k_new.shape or k_new.dtype != v_new.dtype or (
-            k_new.stride(2) != 1 or v_new.stride(2) != 1):
-        raise ValueError("k_new and v_new must be [T, Hkv, d] of one type with contiguous d")
-    sh = _on(dev, stream, v_pages, k_new, v_new, slot, k_scale, v_scale, kbar, err)
-    _ints(slot, "slot", torch.int64, T)
-    _scales(k_scale, v_scale, kv_dtype, Hkv)
-    if kbar is not None:
-        _ints(kbar, "kbar", torch.float32, N, Hkv, d)
-    _call_page("vkv_page_append", _PAGE_APPEND, dev, sh, T, Hkv, d, P, N, _dtype(k_new, "k_new"), kv_dtype, 0,
-               k_new.data_ptr(), 0, k_new.stride(0), k_new.stride(1),
-               v_new.data_ptr(), 0, v_new.stride(0), v_new.stride(1),
-               k_pages.data_ptr(), *k_pages.stride()[:3], v_pages.data_ptr(), *v_pages.stride()[:3],
-               slot.data_ptr(), _ptr(k_scale), _ptr(v_scale), _ptr(kbar), _ptr(err))
+    di = _place(k_pages)
+    N, P, Hkv, d, kv_dtype, cache = _cache(k_pages, v_pages, di)
+    T = k_new.shape[0]
+    if k_new.shape != (T, Hkv, d) or v_new.shape != k_new.shape or k_new.dtype is not v_new.dtype or (
+            k_new.get_device() != di or v_new.get_device() != di):
+        raise ValueError(f"k_new and v_new must be [T, Hkv, d] of one type on cuda:{di}")
+    k0, k1, k2 = k_new.stride()
+    v0, v1, v2 = v_new.stride()
+    if k2 != 1 or v2 != 1:
+        raise ValueError("k_new and v_new must have a contiguous last axis")
+    ks, vs = _scales(k_scale, v_scale, kv_dtype, Hkv, di)
+    _call_page("vkv_page_append", _PAGE_APPEND, di, _handle(di, stream), T, Hkv, d, P, N, _dtype(k_new, "k_new"),
+               kv_dtype, 0, k_new.data_ptr(), 0, k0, k1, v_new.data_ptr(), 0, v0, v1, *cache,
+               _vec(slot, "slot", _I64, (T,), di), ks, vs, _opt(kbar, "kbar", _F32, (N, Hkv, d), di), _err(err, di))
 
 
-def _page_workspace(kept, device, sh, need, clear):
+def _page_workspace(kept, di, sh, need, clear):
     """A workspace of `need` bytes for a call on (device, stream): one kept by this module,
     or, while the stream is being captured, one of the graph's own (two captured graphs
     may be replayed at the same time, so they must not share it)."""
-    if sh != torch._C._cuda_getCurrentRawStream(device.index) or device.index != torch._C._cuda_getDevice():
+    if sh != torch._C._cuda_getCurrentRawStream(di) or di != torch._C._cuda_getDevice():
         # allocate, clear and ask about a capture on the stream that will use it
-        on = torch.cuda.ExternalStream(sh, device=device) if sh else torch.cuda.default_stream(device)
+        on = torch.cuda.ExternalStream(sh, device=di) if sh else torch.cuda.default_stream(di)
         with torch.cuda.stream(on):
-            return _page_workspace(kept, device, sh, need, clear)
-    if torch.cuda.is_current_stream_capturing():
-        return (torch.zeros if clear else torch.empty)(need, dtype=torch.uint8, device=device)
-    key = (device.index, sh)
-    buf = kept.get(key)
+            return _page_workspace(kept, di, sh, need, clear)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return (torch.zeros if clear else torch.empty)(need, dtype=torch.uint8, device=di)
+    buf = kept.get((di, sh))
     if buf is None or buf.numel() < need:
-        buf = (torch.zeros if clear else torch.empty)(need, dtype=torch.uint8, device=device)
-        kept[key] = buf
+        buf = kept[di, sh] = (torch.zeros if clear else torch.empty)(need, dtype=torch.uint8, device=di)
     return buf
+
+
+def _workspace(given, kept, di, sh, need, clear):
+    """(address, bytes) of the caller's workspace, or of one of this module's."""
+    if given is None:
+        return _page_workspace(kept, di, sh, need, clear).data_ptr(), need
+    if given.get_device() != di or not given.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{di}")
+    return given.data_ptr(), given.numel() * given.element_size()
+
+
+def _query(q, what, di):
+    """(address, row stride, head stride) of [R, H, d] with contiguous d."""
+    sb, sh, s1 = q.stride()
+    if s1 != 1 or q.get_device() != di:
+        raise ValueError(f"{what} must be [R, H, d] with contiguous d on cuda:{di}")
+    return q.data_ptr(), sb, 0, sh
 
 
 def page_select(q, kbar, block_table, kv_len, page_size, topk, sink_pages=0, local_pages=0, err=None, stream=None,
@@ -925,22 +952,19 @@ def page_select(q, kbar, block_table, kv_len, page_size, topk, sink_pages=0, loc
     """
     R, H, d = q.shape
     N, Hkv, dk = kbar.shape
-    dev = q.device
+    di = _place(q)
     topk = int(topk)
-    if dk != d or q.stride(2) != 1:
-        raise ValueError("q must be [R, H, d] with contiguous d, kbar [n_pages, Hkv, d]")
-    sel = out if out is not None else torch.empty((R, Hkv, topk), dtype=torch.int32, device=dev)
-    sh = _on(dev, stream, kbar, block_table, kv_len, sel, workspace, err)
-    _ints(kbar, "kbar", torch.float32, N, Hkv, d)
-    _ints(kv_len, "kv_len", torch.int32, R)
-    _ints(sel, "out", torch.int32, R, Hkv, topk)
-    table_stride, W = _page_table(block_table, R), block_table.shape[1]
-    if workspace is None:
-        workspace = _page_workspace(_page_select_ws, dev, sh, vkv_page_select_workspace_size(R, Hkv, W), False)
-    _call_page("vkv_page_select", _PAGE_SELECT, dev, sh, R, H, Hkv, d, int(page_size), N, W, topk, int(sink_pages),
-               int(local_pages), _dtype(q, "q"), 0, q.data_ptr(), q.stride(0), 0, q.stride(1), kbar.data_ptr(),
-               block_table.data_ptr(), table_stride, kv_len.data_ptr(), sel.data_ptr(), workspace.data_ptr(),
-               workspace.numel() * workspace.element_size(), _ptr(err))
+    if dk != d:
+        raise ValueError("q must be [R, H, d], kbar [n_pages, Hkv, d]")
+    sel = out if out is not None else torch.empty((R, Hkv, topk), dtype=_I32, device=di)
+    sh = _handle(di, stream)
+    table, stride, W = _page_table(block_table, R, di)
+    need = 0 if workspace is not None else vkv_page_select_workspace_size(R, Hkv, W)
+    ws = _workspace(workspace, _page_select_ws, di, sh, need, False)
+    _call_page("vkv_page_select", _PAGE_SELECT, di, sh, R, H, Hkv, d, int(page_size), N, W, topk, int(sink_pages),
+               int(local_pages), _dtype(q, "q"), 0, *_query(q, "q", di), _vec(kbar, "kbar", _F32, (N, Hkv, d), di), table,
+               stride, _vec(kv_len, "kv_len", _I32, (R,), di), _vec(sel, "out", _I32, (R, Hkv, topk), di), *ws,
+               _err(err, di))
     return sel
 
 
@@ -955,31 +979,35 @@ def page_attn(q, k_pages, v_pages, block_table, kv_len, scale=None, sink=0, wind
     workspace: a uint8 tensor whose contents were zero before its first use.
     """
     R, H, d = q.shape
-    N, P, Hkv, dk, kv_dtype = _cache(k_pages, v_pages)
-    dev = q.device
-    if dk != d or q.stride(2) != 1:
-        raise ValueError("q must be [R, H, d] with contiguous d, the d of the cache")
+    di = _place(q)
+    N, P, Hkv, dk, kv_dtype, cache = _cache(k_pages, v_pages, di)
+    if dk != d:
+        raise ValueError("q must have the d of the cache")
     if out is None:
-        o, lse = (torch.empty((R, H, d), dtype=q.dtype, device=dev), torch.empty((R, H), dtype=torch.float32, device=dev))
+        o, lse = torch.empty((R, H, d), dtype=q.dtype, device=di), torch.empty((R, H), dtype=_F32, device=di)
     else:
         o, lse = out
-    if o.shape != q.shape or o.dtype != q.dtype or o.stride(2) != 1:
-        raise ValueError("o must have the shape and type of q, with contiguous d")
-    sh = _on(dev, stream, k_pages, v_pages, block_table, kv_len, sel, k_scale, v_scale, o, lse, workspace, err)
-    _ints(kv_len, "kv_len", torch.int32, R)
-    _ints(lse, "lse", torch.float32, R, H)
-    _scales(k_scale, v_scale, kv_dtype, Hkv)
-    topk = 0
+        if o.shape != q.shape or o.dtype is not q.dtype:
+            raise ValueError("o must have the shape and type of q")
+    sh = _handle(di, stream)
+    ks, vs = _scales(k_scale, v_scale, kv_dtype, Hkv, di)
+    table, stride, W = _page_table(block_table, R, di)
+    topk = picked = 0
     if sel is not None:
         topk = sel.shape[-1]
-        _ints(sel, "sel", torch.int32, R, Hkv, topk)
-    table_stride = _page_table(block_table, R)
-    if workspace is None:
-        workspace = _page_workspace(_page_attn_ws, dev, sh, vkv_page_attn_workspace_size(H, Hkv, d), True)
-    _call_page("vkv_page_attn", _PAGE_ATTN, dev, sh, R, H, Hkv, d, P, N, block_table.shape[1], _dtype(q, "q"), kv_dtype,
+        picked = _vec(sel, "sel", _I32, (R, Hkv, topk), di)
+    need = 0 if workspace is not None else _attn_need(H, Hkv, d, di)
+    ws = _workspace(workspace, _page_attn_ws, di, sh, need, True)
+    _call_page("vkv_page_attn", _PAGE_ATTN, di, sh, R, H, Hkv, d, P, N, W, _dtype(q, "q"), kv_dtype,
                float(scale if scale is not None else d ** -0.5), int(sink), int(window), topk, 0,
-               q.data_ptr(), q.stride(0), 0, q.stride(1), o.data_ptr(), o.stride(0), 0, o.stride(1),
-               k_pages.data_ptr(), *k_pages.stride()[:3], v_pages.data_ptr(), *v_pages.stride()[:3],
-               block_table.data_ptr(), table_stride, kv_len.data_ptr(), _ptr(sel), _ptr(k_scale), _ptr(v_scale),
-               lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(err))
+               *_query(q, "q", di), *_query(o, "o", di), *cache, table, stride, _vec(kv_len, "kv_len", _I32, (R,), di),
+               picked, ks, vs, _vec(lse, "lse", _F32, (R, H), di), *ws, _err(err, di))
     return o, lse
+
+
+def _attn_need(H, Hkv, d, di):
+    """vkv_page_attn_workspace_size on device `di` (which depends on its number of SMs)."""
+    if di == torch._C._cuda_getDevice():
+        return vkv_page_attn_workspace_size(H, Hkv, d)
+    with torch.cuda.device(di):
+        return vkv_page_attn_workspace_size(H, Hkv, d)
