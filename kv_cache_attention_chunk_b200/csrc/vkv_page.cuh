@@ -70,6 +70,25 @@ inline FastDiv fast_div(int d) {
   return f;
 }
 
+// Launches a kernel that calls griddep_wait() before it touches memory: its blocks may take
+// their places while the stream's last kernel ends (programmatic dependent launch).
+template <typename P>
+cudaError_t launch_ahead(void (*fn)(const P), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t rc = cudaLaunchKernelEx(&cfg, fn, p);
+  if (rc != cudaSuccess) cudaGetLastError();
+  return rc;
+}
+
 // Bytes of one element.
 inline int dtype_bytes(int dt) { return dt == VKV_E4M3 ? 1 : 2; }
 

@@ -37,13 +37,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlocksPerSm = 2;
-constexpr int kMaxBlocks = kBlocksPerSm * kMaxCtas;
+constexpr int kMaxBlocksPerSm = 3;
+constexpr int kMaxBlocks = kMaxBlocksPerSm * kMaxCtas;
 constexpr float kSlack = 4.f;  // log2: how far a score may exceed the running maximum
-#ifndef VKV_PAGE_MIN_TILES
-#define VKV_PAGE_MIN_TILES 2
-#endif
-constexpr int kMinTiles = VKV_PAGE_MIN_TILES;  // least share of a warp
+// The least share of a warp: short shares spread a small call over more SMs but leave more
+// parts to join (one row of 1560 tokens 14.2 us with 2 tiles, 16.5 with 4; two rows of 64
+// selected pages of 64 tokens 41 and 35 us, selection included)
+constexpr int kMinTiles = 2, kMinTilesLong = 4, kLongUnit = 160;
 
 struct PageAttnParams {
   int R, H, Hkv, G, page, n_pages, W, sink, window, topk;
@@ -67,6 +67,7 @@ struct PageAttnParams {
   int* counters;  // [blocks]
   float* ws_ml;   // [2 * blocks][heads of a chunk][2]: maximum, sum
   float* ws_o;    // [2 * blocks][heads of a chunk][d]
+  float* ws_first;  // [warps][8 or 16 heads][d + 4]: the parts of shares' first units
   int* err;
 };
 
@@ -141,16 +142,23 @@ template <int D, bool F8, int NT>
 struct Shape {
   static constexpr int RB = F8 ? D : 2 * D;        // bytes of a token's row of one head
   static constexpr int CPR = RB / 16;              // 16-byte pieces of it
-  static constexpr int TT = RB == 256 ? 16 : 32;   // tokens per tile: 8 KB of K and V (4 KB for 64-byte rows)
+  // tokens per tile: 8 KB of K and V (4 KB for 64-byte rows).  16 tokens for 128-byte rows, which
+  // would leave room for more warps, cost more per token than these hid (252 against 205 us, and
+  // 214 us with three blocks, on 64 rows of 4096 to 12288 tokens)
+  static constexpr int TT = RB == 256 ? 16 : 32;
   static constexpr int MT = TT / 16;
-  static constexpr int S = NT == 1 ? 3 : 2;        // stages per warp (two blocks' shared memory fits an SM)
+  // blocks per SM and stages per warp.  More warps hide each other's latencies better than
+  // deeper rings (201 against 209 us for 2 blocks of 3 stages on the case above); two chunks'
+  // accumulators leave registers for two blocks
+  static constexpr int BLOCKS = NT == 1 ? 3 : 2;
+  static constexpr int S = NT == 1 ? 2 : 3;
   static constexpr int HC = 8 * NT;                // heads of a chunk
   static constexpr int TILE = TT * RB;             // bytes of K (or V) in a stage
   static constexpr int LD = D + 4;                 // floats between a part's heads (conflict-free accumulator
                                                    // stores); D and D + 1 hold the head's maximum and sum
   static constexpr int PART = HC * LD * 4;         // bytes of a part's O
   static constexpr int WARP = S * 2 * TILE;        // bytes of a warp's ring; a last part is left in it
-  static constexpr int SMEM = kWarps * (WARP + PART);
+  static constexpr int SMEM = kWarps * WARP;
   static_assert(WARP >= PART, "a part fits the ring");
 };
 
@@ -178,6 +186,14 @@ __device__ __forceinline__ long long warp_scan(long long x, int lane) {
   return x;
 }
 
+// Counts one arrival and returns the arrivals before it; what the block has written (seen by
+// this thread through a barrier) is visible to whoever counts after it.
+__device__ __forceinline__ int arrive(int* counter) {
+  int n;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(n) : "l"(counter) : "memory");
+  return n;
+}
+
 struct Part {  // what a warp leaves of a cut unit; valid: te > tb
   int r, u, tb, te, tiles;
   long long unit0;  // the unit's first tile on the line
@@ -186,10 +202,17 @@ struct Part {  // what a warp leaves of a cut unit; valid: te > tb
 // Shares: the line's first `rem` shares have q + 1 tiles, the others q.
 struct Shares {
   long long q, rem;
+  int n;
   __device__ __forceinline__ long long begin(long long w) const { return w * q + min(w, rem); }
-  __device__ __forceinline__ int warp_of(long long x) const {
+  // The share of tile x.  The quotient is below 2^11, so the approximate division is off by
+  // one at most, which is put right; a 64-bit division would take hundreds of cycles.
+  __device__ __forceinline__ int of(long long x) const {
     const long long cut = rem * (q + 1);
-    return (int)(x < cut ? quotient(x, q + 1) : rem + quotient(x - cut, q));
+    int w = x < cut ? (int)__fdividef((float)x, (float)(q + 1)) : (int)(rem + (int)__fdividef((float)(x - cut), (float)q));
+    w = min(w, n - 1);
+    while (begin(w) > x) --w;
+    while (w + 1 < n && begin(w + 1) <= x) ++w;
+    return w;
   }
 };
 
@@ -216,7 +239,7 @@ __device__ __forceinline__ void store_out(T* dst, const float2 a, float f) {
 }
 
 template <int D, typename T, bool F8, int NT>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const PageAttnParams p) {
+__global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_kernel(const PageAttnParams p) {
   using Z = Shape<D, F8, NT>;
   using M = typename std::conditional<F8, __half, T>::type;  // operand type of the products
   // f16 weights use the exponents above 1: with 2^11 for the running maximum, what is below
@@ -224,11 +247,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
   constexpr float kShift = std::is_same<M, __half>::value ? 11.f : 0.f;
   using V4 = typename Vec<D>::type;
   constexpr int VL = D / 32;  // floats of V4
-  extern __shared__ __align__(128) char smem[];
+  extern __shared__ __align__(256) char smem[];
   __shared__ int2 meta[kWarps][Z::S];  // a stage's token mask; row, unit of the row and flags in 12 + 12 + 4 bits
   __shared__ Part parts[2 * kWarps];
-  __shared__ int s_last;
+  __shared__ int4 pending[2];  // row, unit, first block, blocks
+  __shared__ int s_last[2];
 
+  griddep_launch_dependents();
+  griddep_wait();  // launched ahead of the end of the stream's last kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
   const int U = p.Hkv * p.n_chunks;
@@ -259,21 +285,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
   const int per = (p.R + 31) / 32;
   const int r0 = min(p.R, lane * per), r1 = min(p.R, r0 + per);
   long long mine = 0;
-  int len = -1;
+  int len = -1, longest = 0;
   for (int r = r0; r < r1; ++r) {
     len = row_len(r);
     if (len == -2 && p.err && blockIdx.x == 0 && warp == 0) atomicCAS(p.err, 0, VKV_DEVERR_BAD_OFFSETS);
-    mine += row_tiles(len);
+    const int t = row_tiles(len);
+    mine += t;
+    longest = max(longest, t);
   }
   long long before = warp_scan(mine, lane);
   const long long total = __shfl_sync(0xFFFFFFFFu, before, 31) * U;
   before -= mine;
   if (total == 0) return;
-  const long long n_share = min((long long)gridDim.x * kWarps, (total + kMinTiles - 1) / kMinTiles);
+  const int least = __reduce_max_sync(0xFFFFFFFFu, longest) < kLongUnit ? kMinTiles : kMinTilesLong;
+  const long long n_share = min((long long)gridDim.x * kWarps, (total + least - 1) / least);
   if ((long long)blockIdx.x * kWarps >= n_share) return;
   Shares sh;
   sh.q = quotient(total, n_share);
   sh.rem = total - sh.q * n_share;
+  sh.n = (int)n_share;
   const long long my_w = (long long)blockIdx.x * kWarps + warp;
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * Z::WARP);
   if (lane < 2) parts[2 * warp + lane].te = 0;
@@ -364,36 +394,49 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
         }
       }
     };
+    constexpr int ROWS = 32 / Z::CPR;  // rows that the warp copies at once
+    const int row_b = lane / Z::CPR, piece = lane % Z::CPR;
+    auto swizzled = [&](int i) {  // piece_at's offset within row i * ROWS + row_b
+      return Z::RB >= 128 ? (uint32_t)((piece ^ row_b ^ ((i * ROWS) & 7)) << 4) : (uint32_t)((piece ^ ((row_b >> 1) & 3)) << 4);
+    };
     auto issue = [&](int stage) {
       const bool ok = nx_want && nx_page >= 0 && nx_page < p.n_pages;
       if (nx_want && !ok && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
       const unsigned mask = __ballot_sync(0xFFFFFFFFu, ok) & (Z::TT == 32 ? 0xFFFFFFFFu : (1u << Z::TT) - 1u);
       if (lane == 0) meta[warp][stage] = make_int2((int)mask, nx_r << 16 | nx_u << 4 | nx_flags);
       const int h = nx_u / p.n_chunks;
-      const long long ko = ok ? nx_page * p.k_sb + nx_off * p.k_st : 0, vo = ok ? nx_page * p.v_sb + nx_off * p.v_st : 0;
-      const char* kb = p.k + h * p.k_sh;
-      const char* vb = p.v + h * p.v_sh;
-      const uint32_t dk = ring + (uint32_t)(stage * 2 * Z::TILE), dv = dk + Z::TILE;
+      const char* kb = p.k + h * p.k_sh + piece * 16;
+      const char* vb = p.v + h * p.v_sh + piece * 16;
+      const uint32_t dk = ring + (uint32_t)(stage * 2 * Z::TILE) + row_b * Z::RB;
+      // the lane's copies: rows i * ROWS + row_b, one 16-byte piece; a copy of 0 bytes writes
+      // zeros and reads nothing, wherever its source lies
+      const int page0 = __shfl_sync(0xFFFFFFFFu, nx_page, 0), off0 = __shfl_sync(0xFFFFFFFFu, nx_off, 0);
+      if (__all_sync(0xFFFFFFFFu, !ok || (nx_page == page0 && nx_off == off0 + tok_lane))) {
+        // consecutive rows of one page (pages of a multiple of the tile): plain strides
+        const char* sk = kb + (mask & 1u ? page0 * p.k_sb + (off0 + row_b) * p.k_st : 0);
+        const char* sv = vb + (mask & 1u ? page0 * p.v_sb + (off0 + row_b) * p.v_st : 0);
 #pragma unroll
-      for (int i = 0; i < Z::TT * Z::CPR / 32; ++i) {
-        const int row = (i * 32 + lane) / Z::CPR, piece = lane % Z::CPR;
-        const long long rk = __shfl_sync(0xFFFFFFFFu, ko, row), rv = __shfl_sync(0xFFFFFFFFu, vo, row);
-        const int n = (mask >> row) & 1u ? 16 : 0;
-        const uint32_t at = piece_at<Z::RB>(row, piece);
-        cp_async16_zfill(dk + at, kb + rk + piece * 16, n);
-        cp_async16_zfill(dv + at, vb + rv + piece * 16, n);
+        for (int i = 0; i < Z::TT / ROWS; ++i) {
+          const int n = (mask >> (i * ROWS + row_b)) & 1u ? 16 : 0;
+          const uint32_t at = dk + i * ROWS * Z::RB + swizzled(i);
+          cp_async16_zfill(at, sk, n);
+          cp_async16_zfill(at + Z::TILE, sv, n);
+          sk += ROWS * p.k_st;
+          sv += ROWS * p.v_st;
+        }
+      } else {
+        const long long ko = ok ? nx_page * p.k_sb + nx_off * p.k_st : 0, vo = ok ? nx_page * p.v_sb + nx_off * p.v_st : 0;
+#pragma unroll
+        for (int i = 0; i < Z::TT / ROWS; ++i) {
+          const int row = i * ROWS + row_b;
+          const long long rk = __shfl_sync(0xFFFFFFFFu, ko, row), rv = __shfl_sync(0xFFFFFFFFu, vo, row);
+          const int n = (mask >> row) & 1u ? 16 : 0;
+          const uint32_t at = dk + i * ROWS * Z::RB + swizzled(i);
+          cp_async16_zfill(at, kb + rk, n);
+          cp_async16_zfill(at + Z::TILE, vb + rv, n);
+        }
       }
     };
-
-    lookup();
-#pragma unroll
-    for (int s = 0; s < Z::S - 1; ++s) {
-      if (s < count) {
-        issue(s);
-        if (todo > 0) lookup();
-      }
-      cp_async_commit();
-    }
 
     // ---- consume
     uint32_t qf[NT][D / 16][2];
@@ -453,31 +496,40 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
     bool unit_begin = false;
     int stage = 0;
     // ldmatrix row addresses: K pairs (tokens 0-7, 8-15) x (piece, next piece), V the other way round
-    const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_pc = lane >> 4;
-    const int v_row = (lane & 7) + (lane >> 4) * 8, v_pc = (lane >> 3) & 1;
+    const uint32_t k_at = piece_at<Z::RB>((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+    const uint32_t v_at = piece_at<Z::RB>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1) + Z::TILE;
+    // Tile i + S is looked up, tile i + S - 1 fetched and tile i used.  A fetch waits until tile i
+    // has come: with more in flight the memory serves some SMs before others, and the call
+    // waits for the slowest (303 against 281 us for 8 rows of 24 frames)
+    int put = Z::S - 1;  // stage of the tile to fetch
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      __syncwarp();
-      const int2 mt = meta[warp][stage];
+    for (int i = -Z::S; i < count; ++i) {
+      int2 mt = make_int2(0, 0);
+      if (i >= 0) {
+        __syncwarp();
+        mt = meta[warp][stage];
+        const int u = mt.y >> 4 & 4095, h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC;
+        if (mt.y & 1) load_q(mt.y >> 16, h, hc0, min(Z::HC, p.G - hc0));
+        cp_async_wait<Z::S - 2>();
+      }
+      __syncwarp();  // the tile is here, and every lane is done with the stage before it
+      if (i + Z::S - 1 >= 0 && i + Z::S - 1 < count) issue(put);
+      if (todo > 0) lookup();
+      cp_async_commit();
+      put = put + 1 == Z::S ? 0 : put + 1;
+      if (i < 0) continue;
       const unsigned mask = (unsigned)mt.x;
       const int r = mt.y >> 16, u = mt.y >> 4 & 4095, flags = mt.y & 15;
       const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC;  // key head, first query head of the chunk
       const int n_heads = min(Z::HC, p.G - hc0);
-      if (flags & 1) load_q(r, h, hc0, n_heads);
-      cp_async_wait<Z::S - 2>();
-      __syncwarp();
-      if (i + Z::S - 1 < count) {
-        issue(stage == 0 ? Z::S - 1 : stage - 1);
-        if (todo > 0) lookup();
-      }
-      cp_async_commit();
       if (flags & 1) {
         piece_n = 0;
         piece_t0 = i;
         unit_begin = (flags & 4) != 0;
       }
       ++piece_n;
-      const uint32_t sk = ring + (uint32_t)(stage * 2 * Z::TILE), sv = sk + Z::TILE;
+      // piece c of every row: the swizzle and c (even) meet by exclusive or, tiles are aligned to 256 bytes
+      const uint32_t sk = ring + (uint32_t)(stage * 2 * Z::TILE) + k_at, sv = ring + (uint32_t)(stage * 2 * Z::TILE) + v_at;
 
       // ---- scores
       float s[Z::MT][NT][4];
@@ -492,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
 #pragma unroll
         for (int mt2 = 0; mt2 < Z::MT; ++mt2) {
           uint32_t a[4];
-          ldsm4(sk + piece_at<Z::RB>(mt2 * 16 + k_row, c + k_pc), a);
+          ldsm4((sk ^ (uint32_t)(c << 4)) + mt2 * 16 * Z::RB, a);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if constexpr (F8) {
@@ -534,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
             float x = fmaxf(top[nt][e], m[nt][e]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-            const float a = exp2f(m[nt][e] - (x == -INFINITY ? 0.f : x));
+            const float a = ex2_approx(m[nt][e] - (x == -INFINITY ? 0.f : x));
             m[nt][e] = x;
             l[nt][e] *= a;
 #pragma unroll
@@ -568,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
 #pragma unroll
         for (int mt2 = 0; mt2 < Z::MT; ++mt2) {
           uint32_t a[4];
-          ldsm4_t(sv + piece_at<Z::RB>(mt2 * 16 + v_row, c + v_pc), a);
+          ldsm4_t((sv ^ (uint32_t)(c << 4)) + mt2 * 16 * Z::RB, a);
           if constexpr (F8) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -630,11 +682,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
             }
           }
         } else {
-          // a part: the share's first piece goes behind the rings, its last into this warp's ring (all read)
-          const bool is_first = i + 1 == piece_n;
-          const int slot = 2 * warp + (is_first ? 0 : 1);
-          float* po = is_first ? reinterpret_cast<float*>(smem + kWarps * Z::WARP + warp * Z::PART)
-                               : reinterpret_cast<float*>(smem + warp * Z::WARP);
+          // a part: the share's last piece goes into this warp's ring (all of it has been read),
+          // a first piece that others follow to the workspace
+          const bool is_first = i + 1 == piece_n, is_last = i + 1 == count;
+          const int slot = 2 * warp + (is_last ? 1 : 0);
+          float* po = is_last ? reinterpret_cast<float*>(smem + warp * Z::WARP) : p.ws_first + my_w * (Z::HC * Z::LD);
           __syncwarp();
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -675,13 +727,26 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
 
   // ---- join the block's parts; units that go on in other blocks meet in the workspace
   auto part_o = [&](int i) {
-    return reinterpret_cast<const float*>((i & 1) ? smem + (i >> 1) * Z::WARP : smem + kWarps * Z::WARP + (i >> 1) * Z::PART);
+    return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * Z::WARP)
+                   : p.ws_first + ((long long)blockIdx.x * kWarps + (i >> 1)) * (Z::HC * Z::LD);
   };
   const int hcw = min(Z::HC, p.G);  // heads of a workspace part
+  constexpr int HW = Z::HC / kWarps;  // heads of a warp in the joins
+  auto finish = [&](int r, int head, const V4& x, float top, float sum, float vs) {
+    store_out(reinterpret_cast<T*>(p.o) + r * p.o_sb + (long long)head * p.o_sh + lane * VL, x, sum == 0.f ? 0.f : vs / sum);
+    if (lane == 0)
+      p.lse[(size_t)r * p.H + head] =
+          sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - kShift + log2f(sum)) * 0.69314718055994531f;
+  };
   // lane j holds part j (2 w: warp w's first, 2 w + 1: its last); parts of one unit are neighbours
   const int my_part = lane & (2 * kWarps - 1);
   const Part mp = parts[my_part];
   unsigned todo = __ballot_sync(0xFFFFFFFFu, lane < 2 * kWarps && mp.te > 0);
+  int my_b0 = 0, my_n = 0, n_pending = 0;
+  if (todo >> my_part & 1u) {
+    my_b0 = sh.of(mp.unit0) / kWarps;
+    my_n = sh.of(mp.unit0 + mp.tiles - 1) / kWarps - my_b0 + 1;
+  }
 #pragma unroll 1
   while (todo) {
     const int i = __ffs(todo) - 1;
@@ -693,88 +758,124 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
     const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
     const bool whole = tb == 0 && te == tiles;
     const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
-    T* o = reinterpret_cast<T*>(p.o) + r * p.o_sb + (long long)(h * p.G + hc0) * p.o_sh;
-    float* lse = p.lse + (size_t)r * p.H + h * p.G + hc0;
     const size_t ws = (size_t)(2 * blockIdx.x + (tb == 0 ? 1 : 0)) * hcw;
-    for (int hd = warp; hd < n_heads; hd += kWarps) {
-      const float* ml = part_o(my_part) + hd * Z::LD + D;
-      const bool in = grp >> lane & 1u;
-      float top = in ? ml[0] : -INFINITY;
-      const float m = top, l = in ? ml[1] : 0.f;
+    // the warps' parts of this unit (at most one each)
+    const float* src[kWarps];
 #pragma unroll
-      for (int q = 2 * kWarps / 2; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, q));
-      top = __shfl_sync(0xFFFFFFFFu, top, 0);
-      const float base = top == -INFINITY ? 0.f : top;
-      const float wl = exp2f(m - base);
-      float sum = wl * l;
+    for (int w = 0; w < kWarps; ++w) src[w] = part_o(2 * w + (grp >> (2 * w + 1) & 1));
+    float top[HW], sum[HW];
+    V4 x[HW];
 #pragma unroll
-      for (int q = 2 * kWarps / 2; q > 0; q >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, q);
-      sum = __shfl_sync(0xFFFFFFFFu, sum, 0);
-      V4 x;
-      std::memset(&x, 0, sizeof(x));
-      for (unsigned b = grp; b; b &= b - 1) {
-        const int j = __ffs(b) - 1;
-        axpy(x, __shfl_sync(0xFFFFFFFFu, wl, j), *reinterpret_cast<const V4*>(part_o(j) + hd * Z::LD + lane * VL));
+    for (int k = 0; k < HW; ++k) {
+      const int hd = min(warp + k * kWarps, n_heads - 1);
+      float2 ml[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        ml[w] = grp >> (2 * w) & 3 ? *reinterpret_cast<const float2*>(src[w] + hd * Z::LD + D) : make_float2(-INFINITY, 0.f);
+      top[k] = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+      const float base = top[k] == -INFINITY ? 0.f : top[k];
+      sum[k] = 0.f;
+      std::memset(&x[k], 0, sizeof(V4));
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float e = ex2_approx(ml[w].x - base);
+        sum[k] = fmaf(e, ml[w].y, sum[k]);
+        if (grp >> (2 * w) & 3) axpy(x[k], e, *reinterpret_cast<const V4*>(src[w] + hd * Z::LD + lane * VL));
       }
+    }
+#pragma unroll
+    for (int k = 0; k < HW; ++k) {
+      const int hd = warp + k * kWarps;
+      if (hd >= n_heads) break;
       if (whole) {
-        store_out(o + hd * p.o_sh + lane * VL, x, sum == 0.f ? 0.f : vs / sum);
-        if (lane == 0) lse[hd] = sum == 0.f ? -INFINITY : (base - kShift + log2f(sum)) * 0.69314718055994531f;
+        finish(r, h * p.G + hc0 + hd, x[k], top[k], sum[k], vs);
       } else {
-        *reinterpret_cast<V4*>(p.ws_o + (ws + hd) * D + lane * VL) = x;
-        if (lane == 0) *reinterpret_cast<float2*>(p.ws_ml + (ws + hd) * 2) = make_float2(top, sum);
+        *reinterpret_cast<V4*>(p.ws_o + (ws + hd) * D + lane * VL) = x[k];
+        if (lane == 0) *reinterpret_cast<float2*>(p.ws_ml + (ws + hd) * 2) = make_float2(top[k], sum[k]);
       }
     }
-    if (whole) continue;
-    const long long unit0 = __shfl_sync(0xFFFFFFFFu, mp.unit0, i);
-    const int b0 = sh.warp_of(unit0) / kWarps, n = sh.warp_of(unit0 + tiles - 1) / kWarps - b0 + 1;
-    __syncthreads();  // the block's part is written; the fence passes that on
-    if (tid == 0) {
-      __threadfence();
-      s_last = atomicAdd(p.counters + b0, 1) == n - 1;
-      __threadfence();
+    if (!whole) {
+      const int b0 = __shfl_sync(0xFFFFFFFFu, my_b0, i), n = __shfl_sync(0xFFFFFFFFu, my_n, i);
+      if (tid == 0) pending[n_pending] = make_int4(r, u, b0, n);
+      ++n_pending;  // two at most: what began in an earlier block, and what goes on in a later one
     }
-    __syncthreads();
-    if (s_last) {
-      if (tid == 0) p.counters[b0] = 0;
-      for (int hd = warp; hd < n_heads; hd += kWarps) {
-        auto at = [&](int j) { return (size_t)(2 * (b0 + j) + (j == 0 ? 1 : 0)) * hcw + hd; };
-        auto ml = [&](int j) {
-          return j < n ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml + at(j) * 2)) : make_float2(-INFINITY, 0.f);
-        };
-        const float2 ml0 = ml(lane);
-        float top = ml0.x;
-        for (int j = 32 + lane; j < n; j += 32) top = fmaxf(top, ml(j).x);
-#pragma unroll
-        for (int q = 16; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, q));
-        const float base = top == -INFINITY ? 0.f : top;
-        V4 x;
-        std::memset(&x, 0, sizeof(x));
-        float sum = 0.f;
-        for (int j0 = 0; j0 < n; j0 += 32) {
-          const float2 v = j0 == 0 ? ml0 : ml(j0 + lane);
-          const float wl = exp2f(v.x - base);
-          sum = fmaf(wl, v.y, sum);
-          constexpr int kBatch = 16;  // loads in flight
+  }
+  if (n_pending == 0) return;
+  // both units' parts are on their way before either is waited for
+  __syncthreads();  // the block's parts are written; the arrival passes that on
+  if (tid < n_pending) s_last[tid] = arrive(p.counters + pending[tid].z) == pending[tid].w - 1;
+  __syncthreads();
+  if (tid < n_pending && s_last[tid]) p.counters[pending[tid].z] = 0;
+  // The units that this block completes, a warp's heads side by side.  This code runs once per
+  // block and its time is latencies, those of fetching it among them: dealing the heads of both
+  // units to the warps at once, with twice the loads in flight, took 4 us longer
 #pragma unroll 1
-          for (int jb = 0; jb < min(32, n - j0); jb += kBatch) {
-            V4 y[kBatch];
+  for (int f = 0; f < n_pending; ++f) {
+    if (s_last[f]) {
+      const int r = pending[f].x, u = pending[f].y, b0 = pending[f].z, n = pending[f].w;
+      const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
+      const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
+      float top[HW], sum[HW];
+      V4 x[HW];
+      // parts 0 .. n-1, of blocks b0 ..: the unit begins as b0's last part and goes on as the others' first
+      constexpr int kBatch = 8;  // loads in flight per head
+      auto at = [&](int j, int hd) { return (size_t)(2 * (b0 + j) + (j == 0 ? 1 : 0)) * hcw + hd; };
+      V4 y[HW][kBatch];
+      auto load = [&](int j0) {
 #pragma unroll
-            for (int e = 0; e < kBatch; ++e)
-              if (j0 + jb + e < n) y[e] = __ldcg(reinterpret_cast<const V4*>(p.ws_o + at(j0 + jb + e) * D + lane * VL));
+        for (int k = 0; k < HW; ++k)
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e)
+            if (j0 + e < n && warp + k * kWarps < n_heads)
+              y[k][e] = __ldcg(reinterpret_cast<const V4*>(p.ws_o + at(j0 + e, warp + k * kWarps) * D + lane * VL));
+      };
+      auto ml = [&](int j, int k) {
+        return j < n && warp + k * kWarps < n_heads
+                   ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml + at(j, warp + k * kWarps) * 2))
+                   : make_float2(-INFINITY, 0.f);
+      };
+      float2 v[HW];
+#pragma unroll
+      for (int k = 0; k < HW; ++k) v[k] = ml(lane, k);
+      load(0);
+#pragma unroll
+      for (int k = 0; k < HW; ++k) {
+        top[k] = v[k].x;
+        for (int j = 32 + lane; j < n; j += 32) top[k] = fmaxf(top[k], ml(j, k).x);
+#pragma unroll
+        for (int q = 16; q > 0; q >>= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], q));
+        sum[k] = 0.f;
+        std::memset(&x[k], 0, sizeof(V4));
+      }
+#pragma unroll 1
+      for (int j0 = 0; j0 < n; j0 += 32) {
+        float wl[HW];
+#pragma unroll
+        for (int k = 0; k < HW; ++k) {
+          if (j0 > 0) v[k] = ml(j0 + lane, k);
+          wl[k] = ex2_approx(v[k].x - (top[k] == -INFINITY ? 0.f : top[k]));
+          sum[k] = fmaf(wl[k], v[k].y, sum[k]);
+        }
+#pragma unroll 1
+        for (int jb = 0; jb < 32 && j0 + jb < n; jb += kBatch) {
+#pragma unroll
+          for (int k = 0; k < HW; ++k)
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
-              const float w = __shfl_sync(0xFFFFFFFFu, wl, jb + e);
-              if (j0 + jb + e < n) axpy(x, w, y[e]);
+              const float w = __shfl_sync(0xFFFFFFFFu, wl[k], jb + e);
+              if (j0 + jb + e < n) axpy(x[k], w, y[k][e]);
             }
-          }
+          load(j0 + jb + kBatch);
         }
+      }
 #pragma unroll
-        for (int q = 16; q > 0; q >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, q);
-        store_out(o + hd * p.o_sh + lane * VL, x, sum == 0.f ? 0.f : vs / sum);
-        if (lane == 0) lse[hd] = sum == 0.f ? -INFINITY : (base - kShift + log2f(sum)) * 0.69314718055994531f;
+      for (int k = 0; k < HW; ++k) {
+#pragma unroll
+        for (int q = 16; q > 0; q >>= 1) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], q);
+        const int hd = warp + k * kWarps;
+        if (hd < n_heads) finish(r, h * p.G + hc0 + hd, x[k], top[k], sum[k], vs);
       }
     }
-    __syncthreads();  // s_last has been read
   }
 }
 
@@ -782,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) page_attn_kernel(const
 // host
 // ---------------------------------------------------------------------------------------
 template <int D, typename T, bool F8, int NT>
-cudaError_t launch(const PageAttnParams& p, int blocks, int dev, cudaStream_t st) {
+cudaError_t launch(const PageAttnParams& p, int blocks, int n_sm, int dev, cudaStream_t st) {
   using Z = Shape<D, F8, NT>;
   auto fn = page_attn_kernel<D, T, F8, NT>;
   static std::atomic<uint64_t> ready{0};  // devices (by bit) on which the limit is raised
@@ -791,25 +892,27 @@ cudaError_t launch(const PageAttnParams& p, int blocks, int dev, cudaStream_t st
     if (rc != cudaSuccess) return rc;
     ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  fn<<<(unsigned)blocks, kThreads, Z::SMEM, st>>>(p);
-  return cudaGetLastError();
+  return launch_ahead(fn, dim3((unsigned)std::min(blocks, Z::BLOCKS * n_sm)), dim3(kThreads), Z::SMEM, st, p);
 }
 
 template <int D, typename T, bool F8>
-cudaError_t launch_nt(const PageAttnParams& p, int blocks, int dev, cudaStream_t st) {
-  return p.G <= 8 ? launch<D, T, F8, 1>(p, blocks, dev, st) : launch<D, T, F8, 2>(p, blocks, dev, st);
+cudaError_t launch_nt(const PageAttnParams& p, int blocks, int n_sm, int dev, cudaStream_t st) {
+  return p.G <= 8 ? launch<D, T, F8, 1>(p, blocks, n_sm, dev, st) : launch<D, T, F8, 2>(p, blocks, n_sm, dev, st);
 }
 
 template <int D>
-cudaError_t launch_d(const PageAttnParams& p, int q_dtype, int kv_dtype, int blocks, int dev, cudaStream_t st) {
+cudaError_t launch_d(const PageAttnParams& p, int q_dtype, int kv_dtype, int blocks, int n_sm, int dev, cudaStream_t st) {
   if (kv_dtype == VKV_E4M3)
-    return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, true>(p, blocks, dev, st) : launch_nt<D, __half, true>(p, blocks, dev, st);
-  return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, false>(p, blocks, dev, st) : launch_nt<D, __half, false>(p, blocks, dev, st);
+    return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, true>(p, blocks, n_sm, dev, st) : launch_nt<D, __half, true>(p, blocks, n_sm, dev, st);
+  return q_dtype == VKV_BF16 ? launch_nt<D, __nv_bfloat16, false>(p, blocks, n_sm, dev, st) : launch_nt<D, __half, false>(p, blocks, n_sm, dev, st);
 }
 
-// Bytes of the counters and of one block's two workspace parts.
+// Bytes of the counters and of one block's workspace parts.
 constexpr size_t kCounterBytes = (kMaxBlocks * sizeof(int) + 255) / 256 * 256;
-size_t part_bytes(int G, int d) { return (size_t)2 * std::min(G, G <= 8 ? 8 : 16) * (d + 2) * sizeof(float); }
+size_t part_bytes(int G, int d) {
+  const int hc = G <= 8 ? 8 : 16;
+  return ((size_t)2 * std::min(G, hc) * (d + 2) + (size_t)kWarps * hc * (d + 4)) * sizeof(float);
+}
 
 }  // namespace
 }  // namespace vkv
@@ -820,7 +923,7 @@ extern "C" size_t vkv_page_attn_workspace_size(int32_t H, int32_t Hkv, int32_t d
   if (H < 1 || Hkv < 1 || H % Hkv || (d != 64 && d != 128)) return 0;
   const int n_sm = device_sm_count(nullptr);
   if (n_sm <= 0) return 0;
-  const int blocks = std::min(kMaxBlocks, kBlocksPerSm * n_sm);
+  const int blocks = std::min(kMaxBlocks, kMaxBlocksPerSm * n_sm);
   return (kCounterBytes + blocks * part_bytes(H / Hkv, d) + 255) / 256 * 256;
 }
 
@@ -870,10 +973,11 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   p.sel = a->sel;
   p.ks = a->k_scale; p.vs = a->v_scale;
   p.lse = a->lse;
-  const int all = std::min(kMaxBlocks, kBlocksPerSm * n_sm);
+  const int all = std::min(kMaxBlocks, kMaxBlocksPerSm * n_sm);
   p.counters = reinterpret_cast<int*>(a->workspace);
-  p.ws_ml = reinterpret_cast<float*>(reinterpret_cast<char*>(a->workspace) + kCounterBytes);
-  p.ws_o = p.ws_ml + (size_t)2 * all * std::min(p.G, hc) * 2;
+  p.ws_first = reinterpret_cast<float*>(reinterpret_cast<char*>(a->workspace) + kCounterBytes);
+  p.ws_o = p.ws_first + (size_t)all * kWarps * hc * (a->d + 4);
+  p.ws_ml = p.ws_o + (size_t)2 * all * std::min(p.G, hc) * a->d;
   p.err = a->err_word;
   // no more blocks than the longest rows that the table allows could fill
   const int tt = a->d * e == 256 ? 16 : 32;
@@ -883,7 +987,7 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   const long long tiles = ((most + tt - 1) / tt) * a->R * a->Hkv * p.n_chunks;
   const int blocks = (int)std::min<long long>(all, (tiles + kMinTiles * kWarps - 1) / (kMinTiles * kWarps));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t rc = a->d == 128 ? launch_d<128>(p, a->q_dtype, a->kv_dtype, blocks, dev, st)
-                                     : launch_d<64>(p, a->q_dtype, a->kv_dtype, blocks, dev, st);
+  const cudaError_t rc = a->d == 128 ? launch_d<128>(p, a->q_dtype, a->kv_dtype, blocks, n_sm, dev, st)
+                                     : launch_d<64>(p, a->q_dtype, a->kv_dtype, blocks, n_sm, dev, st);
   return rc == cudaSuccess ? VKV_OK : VKV_ERR_CUDA;
 }

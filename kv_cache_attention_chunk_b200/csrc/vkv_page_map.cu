@@ -64,6 +64,8 @@ __device__ __forceinline__ unsigned ring_at(int first, int i, int n) {
 
 template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
   extern __shared__ int sm[];
   int* tok = sm;               // [R + 1] new tokens before row r
   int* need = tok + p.R + 1;   // [R + 1] pages taken before row r
@@ -275,21 +277,25 @@ extern "C" vkv_status vkv_page_map(const vkv_page_map_args* a, vkv_stream_t stre
     cudaGetLastError();
     return VKV_ERR_CUDA;
   }
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!in_place || ctas == 1)  // one block needs no cluster (a cluster launch takes a microsecond more)
+    return launch_ahead(fn, dim3((unsigned)ctas), dim3(kMapThreads), smem, st,
+                        p) == cudaSuccess ? VKV_OK : VKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kMapThreads);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.stream = st;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = (unsigned)ctas;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = in_place ? 1 : 0;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
     cudaGetLastError();
     return VKV_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? VKV_OK : VKV_ERR_CUDA;
+  return VKV_OK;
 }

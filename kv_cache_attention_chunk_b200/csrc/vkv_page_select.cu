@@ -6,6 +6,7 @@
 // queries times fp32 means leave no rounding that could swap two pages whose scores
 // differ in fp32's last bits, whatever the order of the sum.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstring>
 
@@ -15,6 +16,8 @@ namespace vkv {
 namespace {
 
 struct SelParams {
+  FastDiv by_page;
+  int score_steps, head_groups;
   int R, H, Hkv, G, page, n_pages, W, topk, first, last;
   const void* q;
   long long q_sb, q_sh;
@@ -40,81 +43,122 @@ __device__ __forceinline__ double key_value(unsigned long long k) {  // the scor
   return __longlong_as_double((long long)(k ^ ((k >> 63) ? 0x8000000000000000ull : ~0ull)));
 }
 
-constexpr int kScoreThreads = 256;
-constexpr int kScorePer = 2;                                // pages per 8 lanes, loads in flight together
-constexpr int kScorePages = kScorePer * kScoreThreads / 8;  // pages per block
+constexpr int kScoreWarps = 8;
+constexpr int kScoreStages = 3;
+constexpr int kScoreStage = 4096;  // bytes of means that a warp fetches at a time
 
-// grid: x = r * Hkv + g, y = page chunks of the table's width.  8 lanes per page; every
-// load of a block (its means, 512 bytes a page at d = 128) is in flight while the queries
-// are added up.
+// One warp per key head (a block's warps take up to 8 neighbouring heads, whose means lie side
+// by side), 8 lanes per page.  grid: x = row and head group, y = chunks of the table's width
+// (p.score_steps steps of a warp).  HBM-bound (4 d bytes per page and key head): each lane
+// streams the pieces of the means that it will use itself through a private cp.async ring, so
+// that 128 KB per SM are in flight with no registers held and no barriers.  Length, table
+// and queries are asked for together.  The fp64 products hide behind the loads.
 template <int D, typename T>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelParams p) {
-  constexpr int PER = D / 8;  // channels per lane: 4 consecutive of each 32
-  __shared__ double qs[D];
+__global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(const SelParams p) {
+  constexpr int PC = D / 32;                         // 16-byte pieces of a lane per page: 4 channels of each 32
+  constexpr int PASSES = kScoreStage / (4 * 4 * D);  // pages of a lane group per stage
+  constexpr int STEP = 4 * PASSES;                   // pages per step
+  extern __shared__ __align__(16) char ring[];
   griddep_launch_dependents();
-  const int r = blockIdx.x / p.Hkv, g = blockIdx.x - r * p.Hkv;
-  const int len = page_row_len(p.kv_len[r], p.W, p.page, p.err);
-  const int n = len <= 0 ? 0 : (int)(((long long)len + p.page - 1) / p.page);
-  const int j0 = blockIdx.y * kScorePages;
-  if (j0 >= n || n <= p.topk) return;  // all of a short row's pages are kept: no ranking
-  const int sub = threadIdx.x & 7, grp = threadIdx.x >> 3;
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7;
+  const int r = blockIdx.x / p.head_groups, g = (blockIdx.x - r * p.head_groups) * kScoreWarps + warp;
+  if (g >= p.Hkv) return;
+  const int j0 = blockIdx.y * p.score_steps * STEP;
+  const int raw = p.kv_len[r];
   const int* tab = p.table + r * p.table_stride;
-  int pg[kScorePer];
-  float4 v[kScorePer][PER / 4];
+  const int jl = j0 + (lane >> 3);  // the lane's first page
+  int ahead[PASSES];                // table entries of the next step to fetch
 #pragma unroll
-  for (int e = 0; e < kScorePer; ++e) {
-    const int j = j0 + e * (kScoreThreads / 8) + grp;
-    pg[e] = j < n ? tab[j] : -1;
-    if (j < n && (pg[e] < 0 || pg[e] >= p.n_pages)) {
-      if (p.err && sub == 0) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
-      pg[e] = -1;
+  for (int e = 0; e < PASSES; ++e) ahead[e] = jl + e * 4 < p.W ? tab[jl + e * 4] : -1;
+  const T* q = reinterpret_cast<const T*>(p.q) + r * p.q_sb + (long long)g * p.G * p.q_sh + sub * 4;
+  double qr[4 * PC];  // the group's summed queries, at the lane's channels
+#pragma unroll
+  for (int i = 0; i < 4 * PC; ++i) qr[i] = 0.0;
+#pragma unroll 2
+  for (int i = 0; i < p.G; ++i) {
+    uint2 x[PC];
+#pragma unroll
+    for (int c = 0; c < PC; ++c) x[c] = *reinterpret_cast<const uint2*>(q + i * p.q_sh + c * 32);
+#pragma unroll
+    for (int c = 0; c < PC; ++c) {
+      const T* e = reinterpret_cast<const T*>(&x[c]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) qr[4 * c + k] += (double)(float)e[k];
     }
   }
-  const T* q = reinterpret_cast<const T*>(p.q) + r * p.q_sb + (long long)g * p.G * p.q_sh;
-  if (threadIdx.x < D) {
-    double s = 0.0;
-    for (int i = 0; i < p.G; i += 4) {
-      T x[4];
+  const int len = page_row_len(raw, p.W, p.page, p.err);
+  const int n = len <= 0 ? 0 : p.by_page(len) + (p.by_page(len) * p.page < len ? 1 : 0);
+  if (j0 >= n || n <= p.topk) return;  // all of a short row's pages are kept: no ranking
+  const int steps = min(p.score_steps, (n - j0 + STEP - 1) / STEP);
+  const uint32_t mine = smem_u32(ring) + (uint32_t)(warp * kScoreStages * kScoreStage + lane * 16);
+  int pg[kScoreStages][PASSES];  // pages of the steps in flight, the oldest first; -1: none
+  auto fetch = [&](int step, int stage, int* got) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = q[min(i + e, p.G - 1) * p.q_sh + threadIdx.x];
+    for (int e = 0; e < PASSES; ++e) {
+      const int j = jl + step * STEP + e * 4, at = ahead[e];
+      const bool in = step < steps && j < n, ok = in && at >= 0 && at < p.n_pages;
+      if (in && !ok && sub == 0 && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
+      got[e] = ok ? at : -1;
+      if (ok) {
+        const float* src = p.kbar + ((long long)at * p.Hkv + g) * D + sub * 4;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < p.G) s += (double)(float)x[e];
+        for (int i = 0; i < PC; ++i)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + stage * kScoreStage + (e * PC + i) * 512),
+                       "l"(src + i * 32)
+                       : "memory");
+      }
+      const int next = j + STEP;
+      ahead[e] = next < n ? tab[next] : -1;
     }
-    qs[threadIdx.x] = s;
-  }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-  for (int e = 0; e < kScorePer; ++e) {
-    const float4* kb = reinterpret_cast<const float4*>(p.kbar + ((long long)max(pg[e], 0) * p.Hkv + g) * D) + sub;
+  for (int s = 0; s < kScoreStages - 1; ++s) fetch(s, s, pg[s]);
+  unsigned long long* out = p.keys + ((size_t)r * p.Hkv + g) * p.W;
+  int stage = 0;
+#pragma unroll 1
+  for (int step = 0; step < steps; ++step) {
+    const int put = stage == 0 ? kScoreStages - 1 : stage - 1;
+    fetch(step + kScoreStages - 1, put, pg[kScoreStages - 1]);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 1) : "memory");
+    double a[PASSES];
 #pragma unroll
-    for (int i = 0; i < PER / 4; ++i) v[e][i] = pg[e] >= 0 ? __ldg(kb + i * 8) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  __syncthreads();
-  unsigned long long* out = p.keys + (size_t)blockIdx.x * p.W;
+    for (int e = 0; e < PASSES; ++e) a[e] = 0.0;
 #pragma unroll
-  for (int e = 0; e < kScorePer; ++e) {
-    double a = 0.0;
+    for (int i = 0; i < PC; ++i) {
 #pragma unroll
-    for (int i = 0; i < PER / 4; ++i) {
-      const double* qr = qs + i * 32 + sub * 4;
-      a = fma((double)v[e][i].x, qr[0], a);
-      a = fma((double)v[e][i].y, qr[1], a);
-      a = fma((double)v[e][i].z, qr[2], a);
-      a = fma((double)v[e][i].w, qr[3], a);
+      for (int e = 0; e < PASSES; ++e) {
+        const float4 v = *reinterpret_cast<const float4*>(ring + (warp * kScoreStages + stage) * kScoreStage +
+                                                          (e * PC + i) * 512 + lane * 16);
+        a[e] = fma((double)v.x, qr[4 * i], a[e]);
+        a[e] = fma((double)v.y, qr[4 * i + 1], a[e]);
+        a[e] = fma((double)v.z, qr[4 * i + 2], a[e]);
+        a[e] = fma((double)v.w, qr[4 * i + 3], a[e]);
+      }
     }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-    const int j = j0 + e * (kScoreThreads / 8) + grp;
-    if (j < n && sub == 0) {
-      const bool forced = j < p.first || j >= n - p.last;
-      out[j] = forced ? ~0ull : pg[e] >= 0 ? page_key(a) : 0ull;
+    for (int e = 0; e < PASSES; ++e) {
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) a[e] += __shfl_xor_sync(0xFFFFFFFFu, a[e], o);
+      const int j = jl + step * STEP + e * 4;
+      if (j < n && sub == 0) {
+        const bool forced = j < p.first || j >= n - p.last;
+        out[j] = forced ? ~0ull : pg[0][e] >= 0 ? page_key(a[e]) : 0ull;
+      }
     }
+#pragma unroll
+    for (int s = 0; s + 1 < kScoreStages; ++s)
+#pragma unroll
+      for (int e = 0; e < PASSES; ++e) pg[s][e] = pg[s + 1][e];
+    stage = stage + 1 == kScoreStages ? 0 : stage + 1;
   }
 }
 
 constexpr int kPickThreads = 256;
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kHeld = 8;
 constexpr int kCand = 512;  // keys of one bin that are ranked by comparing each with each
 
 // Inclusive sum over the block, in thread order; `total` is the block's sum.
@@ -150,12 +194,13 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
   __shared__ int cand_page[kCand];
   __shared__ int s_bin, s_above, s_in, s_n, s_page;
   __shared__ unsigned long long s_key;
+  griddep_launch_dependents();
   griddep_wait();  // the scores
   const int r = blockIdx.x / p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int raw = p.kv_len[r];
   const int len = (raw >= -1 && (long long)raw <= (long long)p.W * p.page) ? raw : 0;
-  const int n = len <= 0 ? 0 : (int)(((long long)len + p.page - 1) / p.page);
+  const int n = len <= 0 ? 0 : p.by_page(len) + (p.by_page(len) * p.page < len ? 1 : 0);
   int* out = p.sel + (size_t)blockIdx.x * p.topk;
   const int kept = min(n, p.topk);
   for (int i = kept + tid; i < p.topk; i += kPickThreads) out[i] = -1;
@@ -165,18 +210,34 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
     return;
   }
   const unsigned long long* keys = p.keys + (size_t)blockIdx.x * p.W;
+  // thread t has the t-th run of pages, up to kHeld a thread in registers
+  const int per = (n + kPickThreads - 1) / kPickThreads, a = min(n, tid * per), b = min(n, a + per);
+  const bool held = per <= kHeld;
+  unsigned long long own[kHeld];
+  if (held) {
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) own[e] = a + e < b ? keys[a + e] : 0ull;
+  }
+  auto each = [&](auto&& f) {  // f(page, key) for the thread's pages
+    if (held) {
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e)
+        if (a + e < b) f(a + e, own[e]);
+    } else {
+      for (int j = a; j < b; ++j) f(j, keys[j]);
+    }
+  };
   for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
   if (tid == 0) s_n = 0;
   // the finite scores' range
   float lo = INFINITY, hi = -INFINITY;
-  for (int j = tid; j < n; j += kPickThreads) {
-    const unsigned long long k = keys[j];
+  each([&](int, unsigned long long k) {
     const float f = (float)key_value(k);
     if (k != 0ull && k != ~0ull && fabsf(f) < INFINITY) {
       lo = fminf(lo, f);
       hi = fmaxf(hi, f);
     }
-  }
+  });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
@@ -198,7 +259,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
     if (k == ~0ull) return kBins - 1;
     return 1 + max(0, min(kBins - 3, __float2int_rd(((float)key_value(k) - lo) * scale)));
   };
-  for (int j = tid; j < n; j += kPickThreads) atomicAdd(&hist[bin_of(keys[j])], 1);
+  each([&](int, unsigned long long k) { atomicAdd(&hist[bin_of(k)], 1); });
   __syncthreads();
   {  // the bin of the topk-th key: thread t scans bins from the top
     constexpr int B = kBins / kPickThreads;
@@ -220,14 +281,13 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
   const int bin = s_bin, n_in = s_in;
   int need = p.topk - s_above;  // keys of the bin to take: at least one, at most n_in
   if (n_in <= kCand) {
-    for (int j = tid; j < n; j += kPickThreads) {
-      const unsigned long long k = keys[j];
+    each([&](int j, unsigned long long k) {
       if (bin_of(k) == bin) {
         const int at = atomicAdd(&s_n, 1);
         cand_key[at] = k;
         cand_page[at] = j;
       }
-    }
+    });
     __syncthreads();
     for (int i = tid; i < n_in; i += kPickThreads) {
       const unsigned long long k = cand_key[i];
@@ -246,10 +306,9 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
       __syncthreads();
       hist[tid] = 0;
       __syncthreads();
-      for (int j = tid; j < n; j += kPickThreads) {
-        const unsigned long long k = keys[j];
+      each([&](int, unsigned long long k) {
         if ((k & mask) == thr && bin_of(k) == bin) atomicAdd(&hist[(int)(k >> shift) & 255], 1);
-      }
+      });
       __syncthreads();
       int total;
       const int cnt = hist[255 - tid], inc = block_scan(cnt, warp_sum, total);
@@ -262,32 +321,27 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
       mask |= 255ull << shift;
       need -= s_above;
     }
-    // the page of the need-th of the keys equal to it; thread t has the t-th run of pages
-    const int per = (n + kPickThreads - 1) / kPickThreads, a = min(n, tid * per), b = min(n, a + per);
+    // the page of the need-th of the keys equal to it
     int eq = 0, total;
-    for (int j = a; j < b; ++j) eq += keys[j] == thr;
+    each([&](int, unsigned long long k) { eq += k == thr; });
     int before = block_scan(eq, warp_sum, total) - eq;
     if (before < need && need <= before + eq) {
-      for (int j = a; j < b; ++j)
-        if (keys[j] == thr && ++before == need) s_page = j;
+      each([&](int j, unsigned long long k) {
+        if (k == thr && ++before == need) s_page = j;
+      });
       s_key = thr;
     }
   }
   __syncthreads();
-  // ascending output; thread t has the t-th run of pages
+  // ascending output
   const unsigned long long key = s_key;
   const int last = s_page;
-  const int per = (n + kPickThreads - 1) / kPickThreads, a = min(n, tid * per), b = min(n, a + per);
   int mine = 0, total;
-  for (int j = a; j < b; ++j) {
-    const unsigned long long k = keys[j];
-    mine += k > key || (k == key && j <= last);
-  }
+  each([&](int j, unsigned long long k) { mine += k > key || (k == key && j <= last); });
   int at = block_scan(mine, warp_sum, total) - mine;
-  for (int j = a; j < b; ++j) {
-    const unsigned long long k = keys[j];
+  each([&](int j, unsigned long long k) {
     if (k > key || (k == key && j <= last)) out[at++] = j;
-  }
+  });
 }
 
 }  // namespace
@@ -308,7 +362,7 @@ extern "C" vkv_status vkv_page_select(const vkv_page_select_args* a, vkv_stream_
       a->n_pages < 1 || a->W < 1 || a->topk < 1 || a->topk > 4096 || a->sink_pages < 0 || a->local_pages < 0 ||
       (long long)a->sink_pages + a->local_pages > a->topk || a->table_stride < a->W)
     return VKV_ERR_SHAPE;
-  if ((long long)a->R * a->W > INT_MAX || (long long)a->W * a->page > INT_MAX || (long long)a->R * a->Hkv > INT_MAX || a->W > 65535 * kScorePages)
+  if ((long long)a->R * a->W > INT_MAX || (long long)a->W * a->page > INT_MAX || (long long)a->R * a->Hkv > INT_MAX)
     return VKV_ERR_UNSUPPORTED;
   if (!a->q.ptr || !a->kbar || !a->table || !a->kv_len || !a->sel) return VKV_ERR_NULL;
   vkv_tensor q = a->q;
@@ -318,11 +372,13 @@ extern "C" vkv_status vkv_page_select(const vkv_page_select_args* a, vkv_stream_
     return VKV_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return VKV_ERR_ALIGN;
   int dev = 0;
-  if (device_sm_count(&dev) <= 0) return VKV_ERR_CUDA;
+  const int n_sm = device_sm_count(&dev);
+  if (n_sm <= 0) return VKV_ERR_CUDA;
   SelParams p;
   std::memset(&p, 0, sizeof(p));
   p.R = a->R; p.H = a->H; p.Hkv = a->Hkv; p.G = a->H / a->Hkv;
   p.page = a->page; p.n_pages = a->n_pages; p.W = a->W; p.topk = a->topk;
+  p.by_page = fast_div(a->page);
   p.first = a->sink_pages; p.last = a->local_pages;
   p.q = a->q.ptr; p.q_sb = a->q.sb; p.q_sh = a->q.sh;
   p.kbar = a->kbar;
@@ -334,30 +390,30 @@ extern "C" vkv_status vkv_page_select(const vkv_page_select_args* a, vkv_stream_
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int seqs = a->R * a->Hkv;
   if (a->W > a->topk) {
-    const dim3 grid((unsigned)seqs, (unsigned)((a->W + kScorePages - 1) / kScorePages));
+    // steps per warp: about two rounds of the GPU's warps, whose rows end at different places
+    const int step = kScoreStage / (4 * a->d);
+    const long long row_steps = ((long long)a->W + step - 1) / step;
+    const int warps = std::min(kScoreWarps, a->Hkv);
+    p.head_groups = (a->Hkv + kScoreWarps - 1) / kScoreWarps;
+    p.score_steps = (int)std::min<long long>(8, std::max<long long>(1, seqs * row_steps / (2ll * 2 * kScoreWarps * n_sm)));
+    p.score_steps = (int)std::max<long long>(p.score_steps, (row_steps + 65534) / 65535);
+    const dim3 grid((unsigned)(a->R * p.head_groups), (unsigned)((row_steps + p.score_steps - 1) / p.score_steps));
+    const size_t smem = (size_t)warps * kScoreStages * kScoreStage;
     const bool bf = a->q_dtype == VKV_BF16;
-    if (a->d == 128) {
-      if (bf) page_score_kernel<128, __nv_bfloat16><<<grid, kScoreThreads, 0, st>>>(p);
-      else page_score_kernel<128, __half><<<grid, kScoreThreads, 0, st>>>(p);
-    } else {
-      if (bf) page_score_kernel<64, __nv_bfloat16><<<grid, kScoreThreads, 0, st>>>(p);
-      else page_score_kernel<64, __half><<<grid, kScoreThreads, 0, st>>>(p);
+    auto score = a->d == 128 ? (bf ? page_score_kernel<128, __nv_bfloat16> : page_score_kernel<128, __half>)
+                             : (bf ? page_score_kernel<64, __nv_bfloat16> : page_score_kernel<64, __half>);
+    static std::atomic<uint64_t> ready[4];  // by kernel: devices (by bit) on which the shared memory limit is raised
+    std::atomic<uint64_t>& rd = ready[(a->d == 128 ? 2 : 0) + (bf ? 1 : 0)];
+    if (!(rd.load(std::memory_order_acquire) >> dev & 1u)) {
+      if (cudaFuncSetAttribute(score, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kScoreWarps * kScoreStages * kScoreStage) != cudaSuccess) {
+        cudaGetLastError();
+        return VKV_ERR_CUDA;
+      }
+      rd.fetch_or(1ull << dev, std::memory_order_release);
     }
-    if (cudaGetLastError() != cudaSuccess) return VKV_ERR_CUDA;
+    if (launch_ahead(score, grid, dim3((unsigned)warps * 32), smem, st, p) != cudaSuccess) return VKV_ERR_CUDA;
   }
-  // the second kernel's blocks take their places while the first one ends
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)seqs);
-  cfg.blockDim = dim3(kPickThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = a->W > a->topk ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, page_pick_kernel, p) != cudaSuccess) {
-    cudaGetLastError();
-    return VKV_ERR_CUDA;
-  }
-  return VKV_OK;
+  return launch_ahead(page_pick_kernel, dim3((unsigned)seqs), dim3(kPickThreads), 0, st, p) == cudaSuccess ? VKV_OK
+                                                                                                       : VKV_ERR_CUDA;
 }
