@@ -30,37 +30,48 @@ struct AppendParams {
 
 // x / s, correctly rounded: the product with r = 1/s (rounded once) corrected by its exact
 // remainder (Markstein, Computation of elementary functions on the IBM RISC System/6000
-// processor, 1990), which takes half the instructions of a division (e4m3 prompts without means 21 -> 17 us).
-// s outside [2^-60, 2^60], where remainders could underflow, is divided by; quotients of 1e30
-// and more are left as the product (they saturate), and so are infinities and NaN.
+// processor, 1990), two values an instruction, where a division takes about ten.  Chunks with
+// infinities or quotients that could pass 1e30, and s outside [2^-60, 2^60], where remainders
+// could underflow, are divided.
 struct Divisor {
   float s, r;
+  uint64_t s2, r2;  // -s and r, twice each
   bool plain;
   __device__ __forceinline__ explicit Divisor(float scale) {
     s = scale;
     r = __fdiv_rn(1.f, scale);
+    s2 = pack2f(-s, -s);
+    r2 = pack2f(r, r);
     const float a = fabsf(scale);
     plain = !(a >= 0x1p-60f && a <= 0x1p60f);
   }
-  __device__ __forceinline__ void operator()(float* x) const {  // eight values
-    if (plain) {
+  template <typename IN>
+  __device__ __forceinline__ void operator()(const uint4 x, float* f) const {
+    unpack8<IN>(x, f);
+    // the largest magnitude (NaN aside): the sign-free patterns are ordered like the values
+    const uint32_t m01 = __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), m23 = __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu);
+    const uint32_t m = __vmaxu2(m01, m23);
+    float top;
+    {
+      const uint32_t h = max(m >> 16, m & 0xFFFFu);
+      float t[8];
+      unpack8<IN>(make_uint4(h, 0u, 0u, 0u), t);
+      top = t[0];
+    }
+    if (plain || !(top * fabsf(r) < 1e30f)) {
 #pragma unroll 1
-      for (int e = 0; e < 2; ++e) {
-        x[0] = __fdiv_rn(x[0], s), x[1] = __fdiv_rn(x[1], s), x[2] = __fdiv_rn(x[2], s), x[3] = __fdiv_rn(x[3], s);
+      for (int e = 0; e < 8; ++e) {  // rotates, so that no register is indexed
+        const float t = __fdiv_rn(f[0], s);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float t = x[k];
-          x[k] = x[k + 4];
-          x[k + 4] = t;
-        }
+        for (int k = 0; k < 7; ++k) f[k] = f[k + 1];
+        f[7] = t;
       }
       return;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float q = x[e] * r;
-      const float c = fmaf(fmaf(-q, s, x[e]), r, q);
-      x[e] = fabsf(q) < 1e30f ? c : q;
+    for (int e = 0; e < 8; e += 2) {
+      const uint64_t v = pack2f(f[e], f[e + 1]), q = mul2f(v, r2);
+      unpack2f(fma2f(fma2f(q, s2, v), r2, q), f[e], f[e + 1]);
     }
   }
 };
@@ -70,8 +81,7 @@ template <typename IN, bool E4M3>
 __device__ __forceinline__ void store_chunk(char* dst, const uint4 x, const Divisor& by, float* val) {
   if constexpr (E4M3) {
     float f[8];
-    unpack8<IN>(x, f);
-    by(f);
+    by.template operator()<IN>(x, f);
     uint32_t w[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   using V4 = typename Vec<D>::type;
   constexpr int VL = D / 32;  // floats of V4
   extern __shared__ __align__(256) char smem[];
-  __shared__ int2 meta[kWarps][Z::S];  // a stage's token mask; row, unit of the row and flags in 12 + 12 + 4 bits
+  __shared__ int4 meta[kWarps][Z::S];  // of a stage: token mask, row, key head << 16 | chunk of query heads, flags
   __shared__ Part parts[2 * kWarps];
   __shared__ int4 pending[2];  // row, unit, first block, blocks
   __shared__ int s_last[2];
@@ -333,19 +333,21 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     }
     int lo, gap, n_vis = visible(len, lo, gap);
     int tiles = row_tiles(len);
-    int cu = (int)quotient(line0 - row0, tiles), ct = (int)(line0 - row0 - (long long)cu * tiles);
+    const int cu = (int)quotient(line0 - row0, tiles);
+    int ct = (int)(line0 - row0 - (long long)cu * tiles);
+    int chead = cu / p.n_chunks, chunk = cu - chead * p.n_chunks;
     const int ct0 = ct;
     // ---- cursor: the next tile to look up
     int todo = count;  // tiles not yet looked up
     bool first = true;
     const int tok_lane = lane & (Z::TT - 1);
 
-    int nx_page = -1, nx_off = 0, nx_r = 0, nx_u = 0, nx_flags = 0;
+    int nx_page = -1, nx_off = 0, nx_r = 0, nx_hc = 0, nx_flags = 0;
     bool nx_want = false;
     // flags: 1 the share's piece of a unit begins, 2 it ends, 4 the unit begins, 8 the unit ends
     auto lookup = [&]() {
       nx_r = cr;
-      nx_u = cu;
+      nx_hc = chead << 16 | chunk;
       nx_flags = (first || ct == 0 ? 1 : 0) | (todo == 1 || ct == tiles - 1 ? 2 : 0) | (ct == 0 ? 4 : 0) |
                  (ct == tiles - 1 ? 8 : 0);
       first = false;
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
         int j, tok;
         if (p.sel) {
           const int e = p.by_page(x);
-          j = __ldg(p.sel + ((long long)cr * p.Hkv + cu / p.n_chunks) * p.topk + e);
+          j = __ldg(p.sel + ((long long)cr * p.Hkv + chead) * p.topk + e);
           nx_off = x - e * p.page;
           if (j < 0 || j >= p.W) {
             if (j != -1 && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
@@ -375,8 +377,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
       --todo;
       if (++ct == tiles) {
         ct = 0;
-        if (++cu == U && todo > 0) {
-          cu = 0;
+        if (++chunk == p.n_chunks) {
+          chunk = 0;
+          ++chead;
+        }
+        if (chead == p.Hkv && todo > 0) {
+          chead = 0;
           // the next row with tiles: there is one, the line has `todo` more
           int base = cr + 1;
           while (base < p.R) {
@@ -403,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
       const bool ok = nx_want && nx_page >= 0 && nx_page < p.n_pages;
       if (nx_want && !ok && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
       const unsigned mask = __ballot_sync(0xFFFFFFFFu, ok) & (Z::TT == 32 ? 0xFFFFFFFFu : (1u << Z::TT) - 1u);
-      if (lane == 0) meta[warp][stage] = make_int2((int)mask, nx_r << 16 | nx_u << 4 | nx_flags);
-      const int h = nx_u / p.n_chunks;
+      if (lane == 0) meta[warp][stage] = make_int4((int)mask, nx_r, nx_hc, nx_flags);
+      const int h = nx_hc >> 16;
       const char* kb = p.k + h * p.k_sh + piece * 16;
       const char* vb = p.v + h * p.v_sh + piece * 16;
       const uint32_t dk = ring + (uint32_t)(stage * 2 * Z::TILE) + row_b * Z::RB;
@@ -415,10 +421,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
         // consecutive rows of one page (pages of a multiple of the tile): plain strides
         const char* sk = kb + (mask & 1u ? page0 * p.k_sb + (off0 + row_b) * p.k_st : 0);
         const char* sv = vb + (mask & 1u ? page0 * p.v_sb + (off0 + row_b) * p.v_st : 0);
+        const uint32_t there = mask >> row_b;
 #pragma unroll
         for (int i = 0; i < Z::TT / ROWS; ++i) {
-          const int n = (mask >> (i * ROWS + row_b)) & 1u ? 16 : 0;
           const uint32_t at = dk + i * ROWS * Z::RB + swizzled(i);
+          const int n = there >> (i * ROWS) << 4 & 16;
           cp_async16_zfill(at, sk, n);
           cp_async16_zfill(at + Z::TILE, sv, n);
           sk += ROWS * p.k_st;
@@ -504,12 +511,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     int put = Z::S - 1;  // stage of the tile to fetch
 #pragma unroll 1
     for (int i = -Z::S; i < count; ++i) {
-      int2 mt = make_int2(0, 0);
+      int4 mt = make_int4(0, 0, 0, 0);
       if (i >= 0) {
         __syncwarp();
         mt = meta[warp][stage];
-        const int u = mt.y >> 4 & 4095, h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC;
-        if (mt.y & 1) load_q(mt.y >> 16, h, hc0, min(Z::HC, p.G - hc0));
+        if (mt.w & 1) {
+          const int hc0 = (mt.z & 0xFFFF) * Z::HC;
+          load_q(mt.y, mt.z >> 16, hc0, min(Z::HC, p.G - hc0));
+        }
         cp_async_wait<Z::S - 2>();
       }
       __syncwarp();  // the tile is here, and every lane is done with the stage before it
@@ -519,9 +528,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
       put = put + 1 == Z::S ? 0 : put + 1;
       if (i < 0) continue;
       const unsigned mask = (unsigned)mt.x;
-      const int r = mt.y >> 16, u = mt.y >> 4 & 4095, flags = mt.y & 15;
-      const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC;  // key head, first query head of the chunk
-      const int n_heads = min(Z::HC, p.G - hc0);
+      const int flags = mt.w;
       if (flags & 1) {
         piece_n = 0;
         piece_t0 = i;
@@ -560,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
         }
       }
       // ---- weights
+      const bool holes = mask != (Z::TT == 32 ? 0xFFFFFFFFu : (1u << Z::TT) - 1u);
       float top[NT][2];
       bool over = false;
 #pragma unroll
@@ -572,7 +580,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               float& x = s[mt2][nt][2 * hf + e];
-              x = (mask >> (mt2 * 16 + hf * 8 + g8)) & 1u ? x * cs[nt][e] : -INFINITY;
+              x *= cs[nt][e];
+              if (holes && !(mask >> (mt2 * 16 + hf * 8 + g8) & 1u)) x = -INFINITY;
               top[nt][e] = fmaxf(top[nt][e], x);
             }
           over |= top[nt][e] > m[nt][e] + kSlack;
@@ -644,6 +653,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
         }
       }
       if (flags & 2) {
+        const int r = mt.y, h = mt.z >> 16, hc0 = (mt.z & 0xFFFF) * Z::HC;  // row, key head, first query head of the chunk
+        const int n_heads = min(Z::HC, p.G - hc0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -711,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
             const int tb = is_first ? ct0 : 0;
             Part& pt = parts[slot];
             pt.r = r;
-            pt.u = u;
+            pt.u = h * p.n_chunks + (mt.z & 0xFFFF);
             pt.tb = tb;
             pt.te = tb + piece_n;
             pt.tiles = tl;
