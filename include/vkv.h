@@ -520,6 +520,7 @@ typedef enum {
 } vkv_dtype;
 
 #define VKV_PAGE_MAX_ROWS 4096 /* rows of one call */
+#define VKV_PAGE_ATTN_CLEAR_BYTES 4096 /* of vkv_page_attn's workspace, to be cleared once */
 
 /*
  * vkv_page_map -- block table and slot map of one step, from the rows' lengths.
@@ -643,9 +644,10 @@ vkv_status vkv_page_select(const vkv_page_select_args* args, vkv_stream_t stream
  * row's length do not count either).
  * Long rows are split over the key axis and the parts joined by their LSEs, in an order
  * that depends only on the sizes: equal inputs give equal bits.
- * workspace: the first vkv_page_attn_workspace_size() bytes hold the parts and, at the
- * front, counters that have to be zero before the first use and are zero again after each
- * call (clear the buffer once); calls that may overlap on the GPU must not share one.
+ * workspace: vkv_page_attn_workspace_size() bytes for the parts; its first
+ * VKV_PAGE_ATTN_CLEAR_BYTES are counters that have to be zero before the first use and are
+ * zero again after each call (clear them once); calls that may overlap on the GPU must not
+ * share one.
  */
 typedef struct {
   int32_t R, H, Hkv, d;    /* rows; query heads (a multiple of Hkv); key heads; 64 or 128 */

@@ -49,6 +49,7 @@ struct PageAttnParams {
   int R, H, Hkv, G, page, n_pages, W, sink, window, topk;
   FastDiv by_page;
   int n_chunks;                 // chunks of query heads per key head
+  int pair;                     // 1: the line's heads are pairs of key heads (see launch), else 0
   float scale_log2;
   const void* q;
   long long q_sb, q_sh;
@@ -64,9 +65,9 @@ struct PageAttnParams {
   const float* ks;
   const float* vs;
   float* lse;
-  int* counters;  // [blocks]
-  float* ws_ml;   // [2 * blocks][heads of a chunk][2]: maximum, sum
-  float* ws_o;    // [2 * blocks][heads of a chunk][d]
+  int* counters;  // [blocks][2]
+  float* ws_ml;   // [blocks][2][2][heads of a chunk][2]: maximum, sum
+  float* ws_o;    // [blocks][2][2][heads of a chunk][d]
   float* ws_first;  // [warps][8 or 16 heads][d + 4]: the parts of shares' first units
   int* err;
 };
@@ -250,14 +251,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   extern __shared__ __align__(256) char smem[];
   __shared__ int4 meta[kWarps][Z::S];  // of a stage: token mask, row, key head << 16 | chunk of query heads, flags
   __shared__ Part parts[2 * kWarps];
-  __shared__ int4 pending[2];  // row, unit, first block, blocks
-  __shared__ int s_last[2];
+  __shared__ int4 pending[4];
+  __shared__ int s_last[4];
 
   griddep_launch_dependents();
   griddep_wait();  // launched ahead of the end of the stream's last kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
-  const int U = p.Hkv * p.n_chunks;
+  // the line's heads: key heads, or pairs of them, of which an even and an odd warp take one each
+  const int heads = p.Hkv >> p.pair, U = heads * p.n_chunks, sub = warp & p.pair;
+  const int kw = kWarps >> p.pair, kw_log = 2 - p.pair;  // the block's shares
+  static_assert(kWarps == 4, "kw_log");
 
   // a row's visible tokens: x in [0, n) is token x (x < lo) or x + gap, or token x % page of
   // selected page x / page
@@ -298,13 +302,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   before -= mine;
   if (total == 0) return;
   const int least = __reduce_max_sync(0xFFFFFFFFu, longest) < kLongUnit ? kMinTiles : kMinTilesLong;
-  const long long n_share = min((long long)gridDim.x * kWarps, (total + least - 1) / least);
-  if ((long long)blockIdx.x * kWarps >= n_share) return;
+  const long long n_share = min((long long)gridDim.x * kw, quotient(total + least - 1, least));
+  if ((long long)blockIdx.x * kw >= n_share) return;
   Shares sh;
   sh.q = quotient(total, n_share);
   sh.rem = total - sh.q * n_share;
   sh.n = (int)n_share;
-  const long long my_w = (long long)blockIdx.x * kWarps + warp;
+  const long long my_w = (long long)blockIdx.x * kw + (warp >> p.pair);
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * Z::WARP);
   if (lane < 2) parts[2 * warp + lane].te = 0;
   int count = my_w < n_share ? (int)(sh.q + (my_w < sh.rem ? 1 : 0)) : 0;
@@ -347,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     // flags: 1 the share's piece of a unit begins, 2 it ends, 4 the unit begins, 8 the unit ends
     auto lookup = [&]() {
       nx_r = cr;
-      nx_hc = chead << 16 | chunk;
+      const int head = (chead << p.pair) + sub;
+      nx_hc = head << 16 | chunk;
       nx_flags = (first || ct == 0 ? 1 : 0) | (todo == 1 || ct == tiles - 1 ? 2 : 0) | (ct == 0 ? 4 : 0) |
                  (ct == tiles - 1 ? 8 : 0);
       first = false;
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
         int j, tok;
         if (p.sel) {
           const int e = p.by_page(x);
-          j = __ldg(p.sel + ((long long)cr * p.Hkv + chead) * p.topk + e);
+          j = __ldg(p.sel + ((long long)cr * p.Hkv + head) * p.topk + e);
           nx_off = x - e * p.page;
           if (j < 0 || j >= p.W) {
             if (j != -1 && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
           chunk = 0;
           ++chead;
         }
-        if (chead == p.Hkv && todo > 0) {
+        if (chead == heads && todo > 0) {
           chead = 0;
           // the next row with tiles: there is one, the line has `todo` more
           int base = cr + 1;
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
           // a first piece that others follow to the workspace
           const bool is_first = i + 1 == piece_n, is_last = i + 1 == count;
           const int slot = 2 * warp + (is_last ? 1 : 0);
-          float* po = is_last ? reinterpret_cast<float*>(smem + warp * Z::WARP) : p.ws_first + my_w * (Z::HC * Z::LD);
+          float* po = is_last ? reinterpret_cast<float*>(smem + warp * Z::WARP) : p.ws_first + ((long long)blockIdx.x * kWarps + warp) * (Z::HC * Z::LD);
           __syncwarp();
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -755,8 +760,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   unsigned todo = __ballot_sync(0xFFFFFFFFu, lane < 2 * kWarps && mp.te > 0);
   int my_b0 = 0, my_n = 0, n_pending = 0;
   if (todo >> my_part & 1u) {
-    my_b0 = sh.of(mp.unit0) / kWarps;
-    my_n = sh.of(mp.unit0 + mp.tiles - 1) / kWarps - my_b0 + 1;
+    my_b0 = sh.of(mp.unit0) >> kw_log;
+    my_n = (sh.of(mp.unit0 + mp.tiles - 1) >> kw_log) - my_b0 + 1;
   }
 #pragma unroll 1
   while (todo) {
@@ -769,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
     const bool whole = tb == 0 && te == tiles;
     const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
-    const size_t ws = (size_t)(2 * blockIdx.x + (tb == 0 ? 1 : 0)) * hcw;
+    const size_t ws = (((size_t)(2 * blockIdx.x + (tb == 0 ? 1 : 0)) << p.pair) + (h & p.pair)) * hcw;
     // the warps' parts of this unit (at most one each)
     const float* src[kWarps];
 #pragma unroll
@@ -807,30 +812,37 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     }
     if (!whole) {
       const int b0 = __shfl_sync(0xFFFFFFFFu, my_b0, i), n = __shfl_sync(0xFFFFFFFFu, my_n, i);
-      if (tid == 0) pending[n_pending] = make_int4(r, u, b0, n);
-      ++n_pending;  // two at most: what began in an earlier block, and what goes on in a later one
+      // row, key head << 16 | chunk, first block << pair | the head's place in its pair, blocks
+      if (tid == 0) pending[n_pending] = make_int4(r, h << 16 | (u - h * p.n_chunks), b0 << p.pair | (h & p.pair), n);
+      ++n_pending;  // two per head at most: what began in an earlier block, and what goes on in a later one
     }
   }
   if (n_pending == 0) return;
-  // both units' parts are on their way before either is waited for
+  // every unit's parts are on their way before any is waited for
   __syncthreads();  // the block's parts are written; the arrival passes that on
-  if (tid < n_pending) s_last[tid] = arrive(p.counters + pending[tid].z) == pending[tid].w - 1;
+  int* counter = p.counters;  // the unit's, in its first block
+  if (tid < n_pending) {
+    counter += pending[tid].z;
+    s_last[tid] = arrive(counter) == pending[tid].w - 1;
+  }
   __syncthreads();
-  if (tid < n_pending && s_last[tid]) p.counters[pending[tid].z] = 0;
+  if (tid < n_pending && s_last[tid]) *counter = 0;
   // The units that this block completes, a warp's heads side by side.  This code runs once per
   // block and its time is latencies, those of fetching it among them: dealing the heads of both
   // units to the warps at once, with twice the loads in flight, took 4 us longer
 #pragma unroll 1
   for (int f = 0; f < n_pending; ++f) {
     if (s_last[f]) {
-      const int r = pending[f].x, u = pending[f].y, b0 = pending[f].z, n = pending[f].w;
-      const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
+      const int r = pending[f].x, h = pending[f].y >> 16, hc0 = (pending[f].y & 0xFFFF) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
+      const int n = pending[f].w, first = pending[f].z;
       const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
       float top[HW], sum[HW];
       V4 x[HW];
-      // parts 0 .. n-1, of blocks b0 ..: the unit begins as b0's last part and goes on as the others' first
+      // part 0 lies among its block's lasts, the others among their blocks' firsts
       constexpr int kBatch = 8;  // loads in flight per head
-      auto at = [&](int j, int hd) { return (size_t)(2 * (b0 + j) + (j == 0 ? 1 : 0)) * hcw + hd; };
+      const int b0 = first >> p.pair, stride = (2 * hcw) << p.pair;
+      const size_t row1 = (size_t)(b0 + 1) * stride + (first & p.pair) * hcw, row0 = row1 - (hcw << p.pair);
+      auto at = [&](int j, int hd) { return (j == 0 ? row0 : row1 + (size_t)(j - 1) * stride) + hd; };
       V4 y[HW][kBatch];
       auto load = [&](int j0) {
 #pragma unroll
@@ -919,10 +931,11 @@ cudaError_t launch_d(const PageAttnParams& p, int q_dtype, int kv_dtype, int blo
 }
 
 // Bytes of the counters and of one block's workspace parts.
-constexpr size_t kCounterBytes = (kMaxBlocks * sizeof(int) + 255) / 256 * 256;
+constexpr size_t kCounterBytes = VKV_PAGE_ATTN_CLEAR_BYTES;
+static_assert(2 * kMaxBlocks * sizeof(int) <= kCounterBytes, "counters");
 size_t part_bytes(int G, int d) {
   const int hc = G <= 8 ? 8 : 16;
-  return ((size_t)2 * std::min(G, hc) * (d + 2) + (size_t)kWarps * hc * (d + 4)) * sizeof(float);
+  return ((size_t)4 * std::min(G, hc) * (d + 2) + (size_t)kWarps * hc * (d + 4)) * sizeof(float);
 }
 
 }  // namespace
@@ -969,12 +982,16 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   p.R = a->R; p.H = a->H; p.Hkv = a->Hkv; p.G = a->H / a->Hkv;
   p.page = a->page; p.n_pages = a->n_pages; p.W = a->W; p.sink = a->sink; p.window = a->window; p.topk = a->topk;
   p.by_page = fast_div(a->page);
+  const int e = dtype_bytes(a->kv_dtype);
   const int hc = p.G <= 8 ? 8 : 16;
   p.n_chunks = (p.G + hc - 1) / hc;
+  // Rows of 128 bytes or less, one key head's beside the next's: two warps take neighbouring
+  // heads of the same tokens, so that HBM serves runs of twice the length (64 rows of 4096 to
+  // 12288 tokens, e4m3, d = 128: 206 us alone, 192 in pairs).  Selected pages differ by head
+  p.pair = a->d * e <= 128 && !a->sel && a->Hkv % 2 == 0 && a->k.sh == a->d && a->v.sh == a->d ? 1 : 0;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   p.q = a->q.ptr; p.q_sb = a->q.sb; p.q_sh = a->q.sh;
   p.o = a->o.ptr; p.o_sb = a->o.sb; p.o_sh = a->o.sh;
-  const int e = dtype_bytes(a->kv_dtype);
   p.k = reinterpret_cast<const char*>(a->k.ptr);
   p.v = reinterpret_cast<const char*>(a->v.ptr);
   p.k_sb = a->k.sb * e; p.k_st = a->k.st * e; p.k_sh = a->k.sh * e;
@@ -988,7 +1005,7 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   p.counters = reinterpret_cast<int*>(a->workspace);
   p.ws_first = reinterpret_cast<float*>(reinterpret_cast<char*>(a->workspace) + kCounterBytes);
   p.ws_o = p.ws_first + (size_t)all * kWarps * hc * (a->d + 4);
-  p.ws_ml = p.ws_o + (size_t)2 * all * std::min(p.G, hc) * a->d;
+  p.ws_ml = p.ws_o + (size_t)4 * all * std::min(p.G, hc) * a->d;
   p.err = a->err_word;
   // no more blocks than the longest rows that the table allows could fill
   const int tt = a->d * e == 256 ? 16 : 32;

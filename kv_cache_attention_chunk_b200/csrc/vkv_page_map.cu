@@ -46,16 +46,6 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Largest i in [0, n) with cu[i] <= x (cu ascending, cu[0] <= x).
-__device__ __forceinline__ int find_row(const int* cu, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= x) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 // Entry `i` (< n) behind position `first` (< n) of a ring of n < 2^31 entries.
 __device__ __forceinline__ unsigned ring_at(int first, int i, int n) {
   const unsigned x = (unsigned)first + (unsigned)i;
@@ -79,6 +69,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   if (tid == 0) fault = 0;
   const long long taken = p.ring_pos[0], returned = p.ring_pos[1];
   const long long row_cap = (long long)p.W * page;
+  auto pages_of = [&](int n) { return p.by_page(n) + (p.by_page(n) * page < n ? 1 : 0); };
   __syncthreads();
   // each thread: `per` consecutive rows; 64-bit token sum, pages as need | back << 32
   const int per = (R + kMapThreads - 1) / kMapThreads;
@@ -184,29 +175,28 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   if (p.cu)
     for (int r = me; r <= R; r += n_thr) p.cu[r] = bad ? 0 : tok[r];
   const int ring_t = (int)(taken % p.n_ring);
-  if (!bad) {
-    for (int i = me; i < (int)n_need; i += n_thr) {  // new table entries
-      const int r = find_row(need, R, i);
-      const int had = p.by_page(held[r]) + (p.by_page(held[r]) * page < held[r] ? 1 : 0);
-      p.table[r * p.table_stride + had + (i - need[r])] = p.ring[ring_at(ring_t, i, p.n_ring)];
-    }
-    const int ring_b = (int)(returned % p.n_ring);
-    for (int i = me; i < (int)n_back; i += n_thr) {  // pages of ended rows
-      const int r = find_row(back, R, i);
-      p.ring[ring_at(ring_b, i, p.n_ring)] = p.table[r * p.table_stride + (i - back[r])];
-    }
-  }
-  for (long long i0 = me; i0 < p.max_tokens; i0 += (long long)kTok * n_thr) {
-    int row[kTok], t[kTok], pg[kTok];
+  // per step of a thread: one new table entry, one returned page and kTok tokens, whose
+  // bisections and look-ups are all under way before the first result is needed
+  const int ring_b = (int)(returned % p.n_ring);
+  const int taken_n = bad ? 0 : (int)n_need, back_n = bad ? 0 : (int)n_back;
+  const int pages_n = max(taken_n, back_n);
+  long long i0 = me;  // tokens i0, i0 + n_thr, ..
+  for (long long at = me; at < pages_n || i0 < p.max_tokens; at += n_thr, i0 += (long long)kTok * n_thr) {
+    int row[kTok], t[kTok], pg[kTok], rn = 0, rb = 0;
 #pragma unroll
     for (int e = 0; e < kTok; ++e) row[e] = 0;
-    for (int n = R; n > 1;) {  // largest row with tok[row] <= i
+    for (int n = R; n > 1;) {  // the largest row with offset <= item
       const int half = n >> 1;
 #pragma unroll
       for (int e = 0; e < kTok; ++e)
         if (tok[row[e] + half] <= i0 + (long long)e * n_thr) row[e] += half;
+      if (need[rn + half] <= at) rn += half;
+      if (back[rb + half] <= at) rb += half;
       n -= half;
     }
+    int fresh = 0, gone = 0;
+    if (at < taken_n) fresh = p.ring[ring_at(ring_t, (int)at, p.n_ring)];
+    if (at < back_n) gone = p.table[rb * p.table_stride + ((int)at - back[rb])];
 #pragma unroll
     for (int e = 0; e < kTok; ++e) {
       const long long i = i0 + (long long)e * n_thr;
@@ -214,10 +204,12 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
       if (i >= total) continue;
       const int r = row[e], h = held[r];
       t[e] = h + (int)(i - tok[r]);
-      const int j = p.by_page(t[e]), had = p.by_page(h) + (p.by_page(h) * page < h ? 1 : 0);
+      const int j = p.by_page(t[e]), had = pages_of(h);
       pg[e] = j < had ? p.table[r * p.table_stride + j]
                       : p.ring[ring_at(ring_t, need[r] + (j - had), p.n_ring)];
     }
+    if (at < taken_n) p.table[rn * p.table_stride + pages_of(held[rn]) + ((int)at - need[rn])] = fresh;
+    if (at < back_n) p.ring[ring_at(ring_b, (int)at, p.n_ring)] = gone;
 #pragma unroll
     for (int e = 0; e < kTok; ++e) {
       const long long i = i0 + (long long)e * n_thr;

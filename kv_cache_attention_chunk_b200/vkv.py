@@ -32,6 +32,7 @@ MODE_SEGMENTS, MODE_BLOCK_SPARSE, MODE_RAGGED = 0, 1, 2
 MAX_BRANCHES, MAX_SEGMENTS = 2, 8
 DEVERR_TIMEOUT, DEVERR_BAD_INDEX, DEVERR_BAD_OFFSETS, DEVERR_NO_SPACE = 1, 2, 3, 4
 DTYPE_BF16, DTYPE_FP16, DTYPE_E4M3 = 0, 1, 2
+PAGE_ATTN_CLEAR_BYTES = 4096  # VKV_PAGE_ATTN_CLEAR_BYTES in include/vkv.h
 NOALLOC_SCRATCH_BYTES = 4 * 1024 * 1024  # VKV_NOALLOC_SCRATCH_BYTES in include/vkv.h
 STATUS = {0: "VKV_OK", 1: "VKV_ERR_NULL", 2: "VKV_ERR_SHAPE", 3: "VKV_ERR_ALIGN", 4: "VKV_ERR_RANGE",
           5: "VKV_ERR_UNSUPPORTED", 6: "VKV_ERR_CUDA", 7: "VKV_ERR_WORKSPACE"}
@@ -909,6 +910,12 @@ def page_append(k_new, v_new, slot, k_pages, v_pages, k_scale=None, v_scale=None
                _vec(slot, "slot", _I64, (T,), di), ks, vs, _opt(kbar, "kbar", _F32, (N, Hkv, d), di), _err(err, di))
 
 
+def _new_workspace(di, need, clear):
+    buf = torch.empty(need, dtype=torch.uint8, device=di)
+    buf[:clear].zero_()
+    return buf
+
+
 def _page_workspace(kept, di, sh, need, clear):
     """A workspace of `need` bytes for a call on (device, stream): one kept by this module,
     or, while the stream is being captured, one of the graph's own (two captured graphs
@@ -919,10 +926,10 @@ def _page_workspace(kept, di, sh, need, clear):
         with torch.cuda.stream(on):
             return _page_workspace(kept, di, sh, need, clear)
     if torch._C._cuda_isCurrentStreamCapturing():
-        return (torch.zeros if clear else torch.empty)(need, dtype=torch.uint8, device=di)
+        return _new_workspace(di, need, clear)
     buf = kept.get((di, sh))
     if buf is None or buf.numel() < need:
-        buf = kept[di, sh] = (torch.zeros if clear else torch.empty)(need, dtype=torch.uint8, device=di)
+        buf = kept[di, sh] = _new_workspace(di, need, clear)
     return buf
 
 
@@ -960,7 +967,7 @@ def page_select(q, kbar, block_table, kv_len, page_size, topk, sink_pages=0, loc
     sh = _handle(di, stream)
     table, stride, W = _page_table(block_table, R, di)
     need = 0 if workspace is not None else vkv_page_select_workspace_size(R, Hkv, W)
-    ws = _workspace(workspace, _page_select_ws, di, sh, need, False)
+    ws = _workspace(workspace, _page_select_ws, di, sh, need, 0)
     _call_page("vkv_page_select", _PAGE_SELECT, di, sh, R, H, Hkv, d, int(page_size), N, W, topk, int(sink_pages),
                int(local_pages), _dtype(q, "q"), 0, *_query(q, "q", di), _vec(kbar, "kbar", _F32, (N, Hkv, d), di), table,
                stride, _vec(kv_len, "kv_len", _I32, (R,), di), _vec(sel, "out", _I32, (R, Hkv, topk), di), *ws,
@@ -976,7 +983,7 @@ def page_attn(q, k_pages, v_pages, block_table, kv_len, scale=None, sink=0, wind
     float8_e4m3fn with fp32 scales [Hkv]; kv_len int32 [R] (-1: no request, its outputs are
     left as they were).  window > 0 keeps the first `sink` and the last `window` tokens; sel
     (from page_select) the selected pages.  Returns (o [R, H, d], lse fp32 [R, H]).
-    workspace: a uint8 tensor whose contents were zero before its first use.
+    workspace: a uint8 tensor whose first PAGE_ATTN_CLEAR_BYTES were zero before its first use.
     """
     R, H, d = q.shape
     di = _place(q)
@@ -997,7 +1004,7 @@ def page_attn(q, k_pages, v_pages, block_table, kv_len, scale=None, sink=0, wind
         topk = sel.shape[-1]
         picked = _vec(sel, "sel", _I32, (R, Hkv, topk), di)
     need = 0 if workspace is not None else _attn_need(H, Hkv, d, di)
-    ws = _workspace(workspace, _page_attn_ws, di, sh, need, True)
+    ws = _workspace(workspace, _page_attn_ws, di, sh, need, PAGE_ATTN_CLEAR_BYTES)
     _call_page("vkv_page_attn", _PAGE_ATTN, di, sh, R, H, Hkv, d, P, N, W, _dtype(q, "q"), kv_dtype,
                float(scale if scale is not None else d ** -0.5), int(sink), int(window), topk, 0,
                *_query(q, "q", di), *_query(o, "o", di), *cache, table, stride, _vec(kv_len, "kv_len", _I32, (R,), di),
