@@ -7,6 +7,8 @@ then linked into kv_cache_attention_chunk_b200/libvkv.so with the CUDA runtime
 linked statically, so the library loads on machines without a GPU driver.
 The same sources built with VKV_TEST_AIDS defined give libvkv_test.so, the
 test build that also exports the test aids of include/vkv_test.h.
+csrc/vkv_binding.cpp, the paged cache calls' argument marshalling, is built with
+g++ against torch's headers into _binding.so.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +28,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvkv.so")
 LIB_TEST = os.path.join(PKG, "libvkv_test.so")
+BINDING = os.path.join(PKG, "_binding.so")
 TEST_DEFINES = ("VKV_TEST_AIDS",)
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -69,11 +73,12 @@ def _compile(src: str, verbose: bool, defines=(), tag: str = "") -> tuple[str, s
 
 def build(force: bool = False, verbose: bool = False, out: str | None = None, defines=()) -> str:
     """Compile every CUDA source for sm_100a and link libvkv.so and its test build
-    libvkv_test.so; returns the path of libvkv.so.
+    libvkv_test.so, and build the torch binding _binding.so; returns the path of libvkv.so.
 
     `out` / `defines` build one variant library (extra -D macros) at another path.
     """
     if out is None and not defines:
+        _build_binding(force, verbose)
         _build_one(LIB, (), force, verbose)
         _build_one(LIB_TEST, TEST_DEFINES, force, verbose)
         return LIB
@@ -98,6 +103,31 @@ def _build_one(target: str, defines, force: bool, verbose: bool) -> str:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, target)
     return target
+
+
+def _build_binding(force: bool, verbose: bool) -> str:
+    src, deps = os.path.join(CSRC, "vkv_binding.cpp"), [os.path.join(INCLUDE, "vkv.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in [src, *deps]):
+        return BINDING
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cxx = shutil.which("g++")
+    if cxx is None:
+        raise RuntimeError("g++ not found: it is required to build the torch binding")
+    tmp = BINDING + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
+           "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"), src, "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for vkv_binding.cpp:\n" + r.stdout + r.stderr)
+    if verbose:
+        print(r.stdout + r.stderr)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

@@ -1,0 +1,306 @@
+// Argument marshalling of the paged cache calls: torch tensors -> the C structs of vkv.h.
+//
+// These calls run once per layer and token, and their checks (type, shape, place, strides of
+// a dozen tensors) took 4 to 7 us in Python, more than their kernels.  Nothing is computed
+// here: each function checks its tensors, fills the C struct and calls the entry point whose
+// address it is given.  A refused argument is a ValueError; the C status is returned.
+#include <Python.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <exception>
+#include <string>
+
+#include "vkv.h"
+
+namespace {
+
+struct Refusal {
+  std::string text;
+};
+
+const at::Tensor& tensor(PyObject* o, const char* what) {
+  if (!THPVariable_Check(o)) throw Refusal{std::string(what) + " must be a tensor"};
+  return THPVariable_Unpack(o);
+}
+
+std::string place(int dev) { return " on cuda:" + std::to_string(dev); }
+
+int device_of(const at::Tensor& x) {
+  if (!x.is_cuda()) throw Refusal{"expected CUDA tensors"};
+  return x.get_device();
+}
+
+int32_t int_of(PyObject* o, const char* what) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    throw Refusal{std::string(what) + " must be an integer"};
+  }
+  if (v < INT_MIN || v > INT_MAX) throw Refusal{std::string(what) + " is out of range"};
+  return (int32_t)v;
+}
+
+int32_t size_of(int64_t n, const char* what) {
+  if (n > INT_MAX) throw Refusal{std::string(what) + " is out of range"};
+  return (int32_t)n;
+}
+
+// The address of a contiguous tensor of this type and shape on device `dev`; NULL for None where `optional`.
+template <typename T>
+T* vec(PyObject* o, const char* what, at::ScalarType type, at::IntArrayRef shape, int dev, bool optional = false) {
+  if (optional && o == Py_None) return nullptr;
+  const at::Tensor& x = tensor(o, what);
+  if (x.scalar_type() != type || !x.is_cuda() || x.get_device() != dev || x.sizes() != shape || !x.is_contiguous())
+    throw Refusal{std::string(what) + " must be a contiguous " + c10::toString(type) + " tensor of shape " +
+                  c10::str(shape) + place(dev)};
+  return static_cast<T*>(x.data_ptr());
+}
+
+int32_t* err_word(PyObject* o, int dev) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& x = tensor(o, "err");
+  if (x.scalar_type() != at::kInt || !x.is_cuda() || x.get_device() != dev || x.numel() < 1)
+    throw Refusal{"err must be an int32 tensor" + place(dev)};
+  return static_cast<int32_t*>(x.data_ptr());
+}
+
+int32_t dtype_of(const at::Tensor& x, const char* what) {
+  switch (x.scalar_type()) {
+    case at::kBFloat16: return VKV_BF16;
+    case at::kHalf: return VKV_FP16;
+    case at::kFloat8_e4m3fn: return VKV_E4M3;
+    default: throw Refusal{std::string(what) + " is none of bfloat16, float16, float8_e4m3fn"};
+  }
+}
+
+// [.., .., d] with contiguous d: outer and inner stride of a 3-d tensor
+vkv_tensor rows3(const at::Tensor& x, const char* what, int dev, bool outer_is_row) {
+  if (x.dim() != 3 || !x.is_cuda() || x.get_device() != dev || x.stride(2) != 1)
+    throw Refusal{std::string(what) + " must be a 3-d tensor with contiguous last axis" + place(dev)};
+  vkv_tensor t;
+  t.ptr = x.data_ptr();
+  t.sb = outer_is_row ? x.stride(0) : 0;
+  t.st = outer_is_row ? 0 : x.stride(0);
+  t.sh = x.stride(1);
+  return t;
+}
+
+struct Table {
+  int32_t* ptr;
+  int64_t stride;
+  int32_t W;
+};
+Table table_of(PyObject* o, int64_t R, int dev) {
+  const at::Tensor& x = tensor(o, "block_table");
+  if (x.scalar_type() != at::kInt || x.dim() != 2 || !x.is_cuda() || x.get_device() != dev || x.size(0) != R ||
+      (x.size(1) > 1 && x.stride(1) != 1))
+    throw Refusal{"block_table must be an int32 tensor [R, W] with contiguous rows" + place(dev)};
+  // a single row's stride is never used; a narrower one than W means overlapping rows
+  return {static_cast<int32_t*>(x.data_ptr()), R == 1 ? std::max(x.stride(0), x.size(1)) : x.stride(0),
+          size_of(x.size(1), "block_table")};
+}
+
+struct Cache {
+  int32_t n_pages, page, Hkv, d, dtype;
+  vkv_tensor k, v;
+};
+Cache cache_of(PyObject* ko, PyObject* vo, int dev) {
+  const at::Tensor &k = tensor(ko, "k_pages"), &v = tensor(vo, "v_pages");
+  if (k.dim() != 4 || k.sizes() != v.sizes() || k.scalar_type() != v.scalar_type() || !k.is_cuda() || !v.is_cuda() ||
+      k.get_device() != dev || v.get_device() != dev || k.stride(3) != 1 || v.stride(3) != 1)
+    throw Refusal{"k_pages and v_pages must be [n_pages, page, Hkv, d] of one type with contiguous d" + place(dev)};
+  Cache c;
+  c.n_pages = size_of(k.size(0), "n_pages");
+  c.page = size_of(k.size(1), "page");
+  c.Hkv = size_of(k.size(2), "Hkv");
+  c.d = size_of(k.size(3), "d");
+  c.dtype = dtype_of(k, "the cache");
+  c.k = {k.data_ptr(), k.stride(0), k.stride(1), k.stride(2)};
+  c.v = {v.data_ptr(), v.stride(0), v.stride(1), v.stride(2)};
+  return c;
+}
+
+void scales_of(PyObject* ks, PyObject* vs, const Cache& c, int dev, const float** k, const float** v) {
+  *k = *v = nullptr;
+  if (ks == Py_None && vs == Py_None) return;
+  if (c.dtype != VKV_E4M3) throw Refusal{"k_scale and v_scale belong to a float8_e4m3fn cache"};
+  *k = vec<float>(ks, "k_scale", at::kFloat, {c.Hkv}, dev, true);
+  *v = vec<float>(vs, "v_scale", at::kFloat, {c.Hkv}, dev, true);
+}
+
+void workspace_of(PyObject* o, int dev, void** ptr, size_t* bytes) {
+  const at::Tensor& x = tensor(o, "workspace");
+  *ptr = nullptr;
+  *bytes = 0;
+  if (x.numel() == 0) return;  // the entry point says what it needs
+  if (!x.is_cuda() || x.get_device() != dev || !x.is_contiguous())
+    throw Refusal{"workspace must be a contiguous tensor" + place(dev)};
+  *ptr = x.data_ptr();
+  *bytes = x.nbytes();
+}
+
+// (entry point, stream handle) come first in every call
+template <typename A>
+PyObject* call(PyObject* fn, PyObject* stream, const A& a) {
+  using Fn = vkv_status (*)(const A*, vkv_stream_t);
+  Fn f = reinterpret_cast<Fn>(PyLong_AsVoidPtr(fn));
+  vkv_stream_t s = reinterpret_cast<vkv_stream_t>(PyLong_AsVoidPtr(stream));
+  if (PyErr_Occurred()) return nullptr;
+  vkv_status rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = f(&a, s);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong((long)rc);
+}
+
+template <typename F>
+PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F&& body) {
+  if (have != want) {
+    PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, have);
+    return nullptr;
+  }
+  try {
+    return body();
+  } catch (const Refusal& r) {
+    PyErr_SetString(PyExc_ValueError, r.text.c_str());
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+  }
+  return nullptr;
+}
+
+// fn, stream, kv_len, new_len, table, ring, ring_pos, page, max_tokens, out_len, out_ring, slot, row, pos, cu, err
+PyObject* page_map(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded(n, 16, [&]() -> PyObject* {
+    const at::Tensor &len = tensor(x[2], "kv_len"), &ring = tensor(x[5], "ring");
+    const int dev = device_of(len);
+    const int64_t R = len.dim() == 1 ? len.size(0) : -1, n_ring = ring.dim() == 1 ? ring.size(0) : -1;
+    vkv_page_map_args a{};
+    a.R = size_of(R, "kv_len");
+    a.n_ring = size_of(n_ring, "ring");
+    a.page = int_of(x[7], "page_size");
+    a.max_tokens = int_of(x[8], "max_tokens");
+    const Table t = table_of(x[4], R, dev);
+    a.W = t.W;
+    a.table = t.ptr;
+    a.table_stride = t.stride;
+    a.kv_len = vec<int32_t>(x[2], "kv_len", at::kInt, {R}, dev);
+    a.new_len = vec<int32_t>(x[3], "new_len", at::kInt, {R}, dev);
+    a.ring = vec<int32_t>(x[5], "ring", at::kInt, {n_ring}, dev);
+    a.ring_pos = vec<int64_t>(x[6], "ring_pos", at::kLong, {2}, dev);
+    a.kv_len_out = vec<int32_t>(x[9], "out['kv_len']", at::kInt, {R}, dev);
+    a.ring_pos_out = vec<int64_t>(x[10], "out['ring']", at::kLong, {2}, dev);
+    a.slot = vec<int64_t>(x[11], "out['slot']", at::kLong, {a.max_tokens}, dev);
+    a.row = vec<int32_t>(x[12], "out['row']", at::kInt, {a.max_tokens}, dev, true);
+    a.pos = vec<int32_t>(x[13], "out['pos']", at::kInt, {a.max_tokens}, dev, true);
+    a.cu = vec<int32_t>(x[14], "out['cu']", at::kInt, {R + 1}, dev, true);
+    a.err_word = err_word(x[15], dev);
+    return call(x[0], x[1], a);
+  });
+}
+
+// fn, stream, k_new, v_new, slot, k_pages, v_pages, k_scale, v_scale, kbar, err
+PyObject* page_append(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    const at::Tensor &kn = tensor(x[2], "k_new"), &vn = tensor(x[3], "v_new");
+    const int dev = device_of(tensor(x[5], "k_pages"));
+    const Cache c = cache_of(x[5], x[6], dev);
+    if (kn.dim() != 3 || kn.size(1) != c.Hkv || kn.size(2) != c.d || vn.sizes() != kn.sizes() ||
+        kn.scalar_type() != vn.scalar_type())
+      throw Refusal{"k_new and v_new must be [T, Hkv, d] of one type"};
+    vkv_page_append_args a{};
+    a.T = size_of(kn.size(0), "k_new");
+    a.Hkv = c.Hkv, a.d = c.d, a.page = c.page, a.n_pages = c.n_pages;
+    a.x_dtype = dtype_of(kn, "k_new");
+    a.kv_dtype = c.dtype;
+    a.k_new = rows3(kn, "k_new", dev, false);
+    a.v_new = rows3(vn, "v_new", dev, false);
+    a.k = c.k, a.v = c.v;
+    a.slot = vec<int64_t>(x[4], "slot", at::kLong, {a.T}, dev);
+    scales_of(x[7], x[8], c, dev, &a.k_scale, &a.v_scale);
+    a.kbar = vec<float>(x[9], "kbar", at::kFloat, {c.n_pages, c.Hkv, c.d}, dev, true);
+    a.err_word = err_word(x[10], dev);
+    return call(x[0], x[1], a);
+  });
+}
+
+// fn, stream, q, kbar, table, kv_len, page, topk, sink_pages, local_pages, sel, workspace, err
+PyObject* page_select(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* {
+    const at::Tensor &q = tensor(x[2], "q"), &kbar = tensor(x[3], "kbar");
+    const int dev = device_of(q);
+    if (q.dim() != 3 || kbar.dim() != 3 || q.size(2) != kbar.size(2))
+      throw Refusal{"q must be [R, H, d], kbar [n_pages, Hkv, d]"};
+    vkv_page_select_args a{};
+    const int64_t R = q.size(0), Hkv = kbar.size(1);
+    a.R = size_of(R, "q"), a.H = size_of(q.size(1), "q"), a.d = size_of(q.size(2), "q");
+    a.n_pages = size_of(kbar.size(0), "kbar"), a.Hkv = size_of(Hkv, "kbar");
+    a.page = int_of(x[6], "page_size"), a.topk = int_of(x[7], "topk");
+    a.sink_pages = int_of(x[8], "sink_pages"), a.local_pages = int_of(x[9], "local_pages");
+    a.q_dtype = dtype_of(q, "q");
+    a.q = rows3(q, "q", dev, true);
+    a.kbar = vec<float>(x[3], "kbar", at::kFloat, kbar.sizes(), dev);
+    const Table t = table_of(x[4], R, dev);
+    a.table = t.ptr, a.table_stride = t.stride, a.W = t.W;
+    a.kv_len = vec<int32_t>(x[5], "kv_len", at::kInt, {R}, dev);
+    a.sel = vec<int32_t>(x[10], "out", at::kInt, {R, Hkv, a.topk}, dev);
+    workspace_of(x[11], dev, &a.workspace, &a.workspace_bytes);
+    a.err_word = err_word(x[12], dev);
+    return call(x[0], x[1], a);
+  });
+}
+
+// fn, stream, q, k_pages, v_pages, table, kv_len, scale, sink, window, sel, k_scale, v_scale, o, lse, workspace, err
+PyObject* page_attn(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    const at::Tensor &q = tensor(x[2], "q"), &o = tensor(x[13], "o");
+    const int dev = device_of(q);
+    const Cache c = cache_of(x[3], x[4], dev);
+    if (q.dim() != 3 || q.size(2) != c.d) throw Refusal{"q must be [R, H, d], d as in the cache"};
+    if (o.sizes() != q.sizes() || o.scalar_type() != q.scalar_type()) throw Refusal{"o must have the shape and type of q"};
+    vkv_page_attn_args a{};
+    const int64_t R = q.size(0), H = q.size(1);
+    a.R = size_of(R, "q"), a.H = size_of(H, "q");
+    a.Hkv = c.Hkv, a.d = c.d, a.page = c.page, a.n_pages = c.n_pages;
+    a.q_dtype = dtype_of(q, "q");
+    a.kv_dtype = c.dtype;
+    double scale = 1.0 / std::sqrt((double)std::max(c.d, 1));
+    if (x[7] != Py_None) {
+      scale = PyFloat_AsDouble(x[7]);
+      if (PyErr_Occurred()) return nullptr;
+    }
+    a.scale = (float)scale;
+    a.sink = int_of(x[8], "sink"), a.window = int_of(x[9], "window");
+    a.q = rows3(q, "q", dev, true);
+    a.o = rows3(o, "o", dev, true);
+    a.k = c.k, a.v = c.v;
+    const Table t = table_of(x[5], R, dev);
+    a.table = t.ptr, a.table_stride = t.stride, a.W = t.W;
+    a.kv_len = vec<int32_t>(x[6], "kv_len", at::kInt, {R}, dev);
+    if (x[10] != Py_None) {
+      const at::Tensor& sel = tensor(x[10], "sel");
+      a.topk = size_of(sel.dim() == 3 ? sel.size(2) : -1, "sel");
+      a.sel = vec<int32_t>(x[10], "sel", at::kInt, {R, c.Hkv, a.topk}, dev);
+    }
+    scales_of(x[11], x[12], c, dev, &a.k_scale, &a.v_scale);
+    a.lse = vec<float>(x[14], "lse", at::kFloat, {R, H}, dev);
+    workspace_of(x[15], dev, &a.workspace, &a.workspace_bytes);
+    a.err_word = err_word(x[16], dev);
+    return call(x[0], x[1], a);
+  });
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
+}
+PyMethodDef methods[] = {method<page_map>("page_map"), method<page_append>("page_append"),
+                         method<page_select>("page_select"), method<page_attn>("page_attn"), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }

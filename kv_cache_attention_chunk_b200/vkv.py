@@ -1,4 +1,5 @@
-"""ctypes binding of libvkv (include/vkv.h): argument marshalling only.
+"""ctypes binding of libvkv (include/vkv.h): argument marshalling only (the paged cache
+calls' in csrc/vkv_binding.cpp).
 
 Every computation runs in the library's sm_100a kernels; this module turns
 torch tensors into the C structs, passes the current CUDA stream and raises
@@ -18,8 +19,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
-import struct
 from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import numpy as np
@@ -257,8 +258,10 @@ def _load(path: str) -> ctypes.CDLL:
     L.vkv_latent_attn.restype = c_int32
     for name in ("vkv_page_map", "vkv_page_append", "vkv_page_select", "vkv_page_attn"):
         fn = getattr(L, name)
-        fn.argtypes = [c_void_p, c_void_p]  # a struct by reference, or its packed bytes
+        fn.argtypes = [c_void_p, c_void_p]
         fn.restype = c_int32
+    L.page_entry = {name: ctypes.cast(getattr(L, "vkv_" + name), c_void_p).value
+                    for name in ("page_map", "page_append", "page_select", "page_attn")}
     L.vkv_page_select_workspace_size.argtypes = [c_int32] * 3
     L.vkv_page_select_workspace_size.restype = c_size_t
     L.vkv_page_attn_workspace_size.argtypes = [c_int32] * 3
@@ -750,109 +753,48 @@ def latent_attn(q, kv, d_c, scale=None, kr=None, err=None, stream=None, out=None
 # ---------------------------------------------------------------------------
 # paged cache: one query per row (request) over pages of tokens
 # ---------------------------------------------------------------------------
-# These calls run once per layer and token, so their arguments are packed by struct
-# (the C layout, checked against the ctypes structures) instead of field by field.
-_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float8_e4m3fn: DTYPE_E4M3}
-_T = "Pqqq"  # a vkv_tensor
-_PAGE_MAP = struct.Struct("@6i3Pq9P")
-_PAGE_APPEND = struct.Struct("@8i" + 4 * _T + "5P")
-_PAGE_SELECT = struct.Struct("@12i" + _T + "PPqPPPNP")
-_PAGE_ATTN = struct.Struct("@9if4i" + 4 * _T + "PqPPPPPPNP")
-for _fmt, _cls in ((_PAGE_MAP, vkv_page_map_args), (_PAGE_APPEND, vkv_page_append_args),
-                   (_PAGE_SELECT, vkv_page_select_args), (_PAGE_ATTN, vkv_page_attn_args)):
-    if _fmt.size != ctypes.sizeof(_cls):
-        raise RuntimeError(f"packed layout of {_cls.__name__}: {_fmt.size} B, expected {ctypes.sizeof(_cls)} B")
-
+# These calls run once per layer and token; their arguments are checked and marshalled by
+# csrc/vkv_binding.cpp (a refused one is a ValueError), which calls the same entry points.
 _page_attn_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, cleared once (the call leaves it clear)
+_NO_WORKSPACE = torch.empty(0, dtype=torch.uint8)
 _page_select_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, grown on demand
 
 
-_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_binding = None
+
+
+def _page_binding():
+    global _binding
+    if _binding is None:
+        try:
+            from . import _binding as b
+        except ImportError as e:
+            raise RuntimeError(f"the torch binding does not load ({e}): build it with "
+                               "`python -m kv_cache_attention_chunk_b200.build`") from e
+        _binding = b
+    return _binding
+
+
+def _page_call(name, x, stream, *args):
+    """One call on the device of `x`: with it current, on `stream`; raises VkvError on a non-OK status."""
+    fn = getattr(_binding or _page_binding(), name)
+    address = (_lib or lib()).page_entry[name]
+    di = x.get_device()
+    sh = _handle(di, stream)
+    if di < 0 or di == torch._C._cuda_getDevice():
+        status = fn(address, sh, *args)
+    else:
+        with torch.cuda.device(di):
+            status = fn(address, sh, *args)
+    if status:
+        _check(status, "vkv_" + name)
 
 
 def _handle(di, stream):
-    """The stream handle for a call on device `di`."""
+    """The stream handle for a call on device `di` (-1, no GPU tensor: refused by the call)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(di)
+        return torch._C._cuda_getCurrentRawStream(di) if di >= 0 else 0
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _call_page(name, fmt, di, sh, *values):
-    """One C call with device `di` current; raises VkvError on a non-OK status."""
-    fn = getattr(_lib or lib(), name)
-    if di == torch._C._cuda_getDevice():
-        status = fn(fmt.pack(*values), sh)
-    else:
-        with torch.cuda.device(di):
-            status = fn(fmt.pack(*values), sh)
-    if status:
-        _check(status, name)
-
-
-def _place(x):
-    di = x.get_device()
-    if di < 0:
-        raise ValueError("expected CUDA tensors")
-    return di
-
-
-def _vec(x, what, dtype, shape, di):
-    """The address of `x`, checked to be a contiguous `dtype` tensor of `shape` on device `di`."""
-    if x.dtype is not dtype or x.shape != shape or x.get_device() != di or not x.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on cuda:{di}, got {x.dtype} "
-                         f"{tuple(x.shape)} on {x.device}")
-    return x.data_ptr()
-
-
-def _opt(x, what, dtype, shape, di):
-    return 0 if x is None else _vec(x, what, dtype, shape, di)
-
-
-def _err(err, di):
-    if err is None:
-        return 0
-    if err.dtype is not _I32 or err.get_device() != di or err.numel() < 1:
-        raise ValueError(f"err must be an int32 tensor on cuda:{di}")
-    return err.data_ptr()
-
-
-def _page_table(table, R, di):
-    """(address, row stride, columns) of a block table."""
-    if table.dtype is not _I32 or table.ndim != 2 or table.get_device() != di:
-        raise ValueError(f"block_table must be an int32 tensor [R, W] on cuda:{di}")
-    rows, W = table.shape
-    stride, inner = table.stride()
-    if rows != R or (W > 1 and inner != 1):
-        raise ValueError("block_table must be an int32 tensor [R, W] with contiguous rows")
-    # a single row's stride is never used; a narrower one than W means overlapping rows
-    return table.data_ptr(), max(stride, W) if R == 1 else stride, W
-
-
-def _cache(k, v, di):
-    """(pages, tokens per page, key heads, d, dtype code, k's and v's vkv_tensor fields) of a paged cache pair."""
-    N, P, Hkv, d = shape = k.shape
-    if shape != v.shape or k.dtype is not v.dtype or k.get_device() != di or v.get_device() != di:
-        raise ValueError(f"k_pages and v_pages must be [n_pages, page, Hkv, d] of one type on cuda:{di}")
-    k0, k1, k2, k3 = k.stride()
-    v0, v1, v2, v3 = v.stride()
-    if k3 != 1 or v3 != 1:
-        raise ValueError("k_pages and v_pages must have a contiguous last axis")
-    return N, P, Hkv, d, _dtype(k, "the cache"), (k.data_ptr(), k0, k1, k2, v.data_ptr(), v0, v1, v2)
-
-
-def _dtype(x, what):
-    try:
-        return _DTYPES[x.dtype]
-    except KeyError:
-        raise ValueError(f"{what}: {x.dtype} is not one of bfloat16, float16, float8_e4m3fn") from None
-
-
-def _scales(k_scale, v_scale, kv_dtype, Hkv, di):
-    if k_scale is None and v_scale is None:
-        return 0, 0
-    if kv_dtype != DTYPE_E4M3:
-        raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache")
-    return _opt(k_scale, "k_scale", _F32, (Hkv,), di), _opt(v_scale, "v_scale", _F32, (Hkv,), di)
 
 
 def page_map(kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens, out=None, err=None, stream=None):
@@ -866,24 +808,14 @@ def page_map(kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens
     missing); out["kv_len"] may be kv_len itself and out["ring"] ring_pos.  A step that does
     not fit changes nothing and sets err.
     """
-    R, di = kv_len.shape[0], _place(kv_len)
-    max_tokens = int(max_tokens)
     if out is None:
-        dev = kv_len.device
-        out = {"kv_len": torch.empty(R, dtype=_I32, device=dev), "ring": torch.empty(2, dtype=_I64, device=dev),
-               "slot": torch.empty(max_tokens, dtype=_I64, device=dev),
-               "row": torch.empty(max_tokens, dtype=_I32, device=dev),
-               "pos": torch.empty(max_tokens, dtype=_I32, device=dev), "cu": torch.empty(R + 1, dtype=_I32, device=dev)}
-    table, stride, W = _page_table(block_table, R, di)
-    rows, tokens, n_ring = (R,), (max_tokens,), ring.shape[0]
+        R, i32, i64 = kv_len.shape[0], dict(dtype=torch.int32, device=kv_len.device), dict(dtype=torch.int64, device=kv_len.device)
+        out = {"kv_len": torch.empty(R, **i32), "ring": torch.empty(2, **i64), "slot": torch.empty(max_tokens, **i64),
+               "row": torch.empty(max_tokens, **i32), "pos": torch.empty(max_tokens, **i32),
+               "cu": torch.empty(R + 1, **i32)}
     get = out.get
-    _call_page("vkv_page_map", _PAGE_MAP, di, _handle(di, stream), R, W, int(page_size), n_ring, max_tokens, 0,
-               _vec(kv_len, "kv_len", _I32, rows, di), _vec(new_len, "new_len", _I32, rows, di), table, stride,
-               _vec(ring, "ring", _I32, (n_ring,), di), _vec(ring_pos, "ring_pos", _I64, (2,), di),
-               _vec(out["kv_len"], "out['kv_len']", _I32, rows, di), _vec(out["ring"], "out['ring']", _I64, (2,), di),
-               _vec(out["slot"], "out['slot']", _I64, tokens, di), _opt(get("row"), "out['row']", _I32, tokens, di),
-               _opt(get("pos"), "out['pos']", _I32, tokens, di), _opt(get("cu"), "out['cu']", _I32, (R + 1,), di),
-               _err(err, di))
+    _page_call("page_map", kv_len, stream, kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens,
+               out["kv_len"], out["ring"], out["slot"], get("row"), get("pos"), get("cu"), err)
     return out
 
 
@@ -894,20 +826,7 @@ def page_append(k_new, v_new, slot, k_pages, v_pages, k_scale=None, v_scale=None
     x / scale, fp32 scales [Hkv]); kbar (optional fp32 [n_pages, Hkv, d]) receives the key
     mean of each page written to.
     """
-    di = _place(k_pages)
-    N, P, Hkv, d, kv_dtype, cache = _cache(k_pages, v_pages, di)
-    T = k_new.shape[0]
-    if k_new.shape != (T, Hkv, d) or v_new.shape != k_new.shape or k_new.dtype is not v_new.dtype or (
-            k_new.get_device() != di or v_new.get_device() != di):
-        raise ValueError(f"k_new and v_new must be [T, Hkv, d] of one type on cuda:{di}")
-    k0, k1, k2 = k_new.stride()
-    v0, v1, v2 = v_new.stride()
-    if k2 != 1 or v2 != 1:
-        raise ValueError("k_new and v_new must have a contiguous last axis")
-    ks, vs = _scales(k_scale, v_scale, kv_dtype, Hkv, di)
-    _call_page("vkv_page_append", _PAGE_APPEND, di, _handle(di, stream), T, Hkv, d, P, N, _dtype(k_new, "k_new"),
-               kv_dtype, 0, k_new.data_ptr(), 0, k0, k1, v_new.data_ptr(), 0, v0, v1, *cache,
-               _vec(slot, "slot", _I64, (T,), di), ks, vs, _opt(kbar, "kbar", _F32, (N, Hkv, d), di), _err(err, di))
+    _page_call("page_append", k_pages, stream, k_new, v_new, slot, k_pages, v_pages, k_scale, v_scale, kbar, err)
 
 
 def _new_workspace(di, need, clear):
@@ -920,6 +839,8 @@ def _page_workspace(kept, di, sh, need, clear):
     """A workspace of `need` bytes for a call on (device, stream): one kept by this module,
     or, while the stream is being captured, one of the graph's own (two captured graphs
     may be replayed at the same time, so they must not share it)."""
+    if di < 0 or need <= 0:
+        return _NO_WORKSPACE  # what makes the call refuse its arguments comes first
     if sh != torch._C._cuda_getCurrentRawStream(di) or di != torch._C._cuda_getDevice():
         # allocate, clear and ask about a capture on the stream that will use it
         on = torch.cuda.ExternalStream(sh, device=di) if sh else torch.cuda.default_stream(di)
@@ -933,23 +854,6 @@ def _page_workspace(kept, di, sh, need, clear):
     return buf
 
 
-def _workspace(given, kept, di, sh, need, clear):
-    """(address, bytes) of the caller's workspace, or of one of this module's."""
-    if given is None:
-        return _page_workspace(kept, di, sh, need, clear).data_ptr(), need
-    if given.get_device() != di or not given.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{di}")
-    return given.data_ptr(), given.numel() * given.element_size()
-
-
-def _query(q, what, di):
-    """(address, row stride, head stride) of [R, H, d] with contiguous d."""
-    sb, sh, s1 = q.stride()
-    if s1 != 1 or q.get_device() != di:
-        raise ValueError(f"{what} must be [R, H, d] with contiguous d on cuda:{di}")
-    return q.data_ptr(), sb, 0, sh
-
-
 def page_select(q, kbar, block_table, kv_len, page_size, topk, sink_pages=0, local_pages=0, err=None, stream=None,
                 out=None, workspace=None):
     """The `topk` pages that each row and key head attends to (vkv_page_select).
@@ -957,21 +861,14 @@ def page_select(q, kbar, block_table, kv_len, page_size, topk, sink_pages=0, loc
     q [R, H, d]; kbar fp32 [n_pages, Hkv, d], the pages' key means (page_append keeps them).
     Returns int32 [R, Hkv, topk]: logical page numbers ascending, then -1.
     """
-    R, H, d = q.shape
-    N, Hkv, dk = kbar.shape
-    di = _place(q)
-    topk = int(topk)
-    if dk != d:
-        raise ValueError("q must be [R, H, d], kbar [n_pages, Hkv, d]")
-    sel = out if out is not None else torch.empty((R, Hkv, topk), dtype=_I32, device=di)
-    sh = _handle(di, stream)
-    table, stride, W = _page_table(block_table, R, di)
-    need = 0 if workspace is not None else vkv_page_select_workspace_size(R, Hkv, W)
-    ws = _workspace(workspace, _page_select_ws, di, sh, need, 0)
-    _call_page("vkv_page_select", _PAGE_SELECT, di, sh, R, H, Hkv, d, int(page_size), N, W, topk, int(sink_pages),
-               int(local_pages), _dtype(q, "q"), 0, *_query(q, "q", di), _vec(kbar, "kbar", _F32, (N, Hkv, d), di), table,
-               stride, _vec(kv_len, "kv_len", _I32, (R,), di), _vec(sel, "out", _I32, (R, Hkv, topk), di), *ws,
-               _err(err, di))
+    R, Hkv = q.shape[0], kbar.shape[1]
+    sel = out if out is not None else torch.empty((R, Hkv, topk), dtype=torch.int32, device=q.device)
+    if workspace is None:
+        di = q.get_device()
+        workspace = _page_workspace(_page_select_ws, di, _handle(di, stream),
+                                    vkv_page_select_workspace_size(R, Hkv, block_table.shape[1]), 0)
+    _page_call("page_select", q, stream, q, kbar, block_table, kv_len, page_size, topk, sink_pages, local_pages, sel,
+               workspace, err)
     return sel
 
 
@@ -986,35 +883,20 @@ def page_attn(q, k_pages, v_pages, block_table, kv_len, scale=None, sink=0, wind
     workspace: a uint8 tensor whose first PAGE_ATTN_CLEAR_BYTES were zero before its first use.
     """
     R, H, d = q.shape
-    di = _place(q)
-    N, P, Hkv, dk, kv_dtype, cache = _cache(k_pages, v_pages, di)
-    if dk != d:
-        raise ValueError("q must have the d of the cache")
     if out is None:
-        o, lse = torch.empty((R, H, d), dtype=q.dtype, device=di), torch.empty((R, H), dtype=_F32, device=di)
-    else:
-        o, lse = out
-        if o.shape != q.shape or o.dtype is not q.dtype:
-            raise ValueError("o must have the shape and type of q")
-    sh = _handle(di, stream)
-    ks, vs = _scales(k_scale, v_scale, kv_dtype, Hkv, di)
-    table, stride, W = _page_table(block_table, R, di)
-    topk = picked = 0
-    if sel is not None:
-        topk = sel.shape[-1]
-        picked = _vec(sel, "sel", _I32, (R, Hkv, topk), di)
-    need = 0 if workspace is not None else _attn_need(H, Hkv, d, di)
-    ws = _workspace(workspace, _page_attn_ws, di, sh, need, PAGE_ATTN_CLEAR_BYTES)
-    _call_page("vkv_page_attn", _PAGE_ATTN, di, sh, R, H, Hkv, d, P, N, W, _dtype(q, "q"), kv_dtype,
-               float(scale if scale is not None else d ** -0.5), int(sink), int(window), topk, 0,
-               *_query(q, "q", di), *_query(o, "o", di), *cache, table, stride, _vec(kv_len, "kv_len", _I32, (R,), di),
-               picked, ks, vs, _vec(lse, "lse", _F32, (R, H), di), *ws, _err(err, di))
+        out = torch.empty((R, H, d), dtype=q.dtype, device=q.device), torch.empty((R, H), dtype=torch.float32, device=q.device)
+    o, lse = out
+    if workspace is None:
+        di = q.get_device()
+        workspace = _page_workspace(_page_attn_ws, di, _handle(di, stream), _attn_need(H, k_pages.shape[2], d, di),
+                                    PAGE_ATTN_CLEAR_BYTES)
+    _page_call("page_attn", q, stream, q, k_pages, v_pages, block_table, kv_len, scale, sink, window, sel, k_scale, v_scale,
+               o, lse, workspace, err)
     return o, lse
 
 
+@functools.lru_cache(maxsize=256)
 def _attn_need(H, Hkv, d, di):
-    """vkv_page_attn_workspace_size on device `di` (which depends on its number of SMs)."""
-    if di == torch._C._cuda_getDevice():
-        return vkv_page_attn_workspace_size(H, Hkv, d)
+    """vkv_page_attn_workspace_size on device `di` (it depends on the sizes and the device's SMs)."""
     with torch.cuda.device(di):
         return vkv_page_attn_workspace_size(H, Hkv, d)
