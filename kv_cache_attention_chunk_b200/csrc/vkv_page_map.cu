@@ -52,6 +52,11 @@ __device__ __forceinline__ unsigned ring_at(int first, int i, int n) {
   return x >= (unsigned)n ? x - (unsigned)n : x;
 }
 
+// Where position t of a ring of n lies; a 64-bit remainder only once t has passed 2^32.
+__device__ __forceinline__ int ring_start(long long t, int n) {
+  return (unsigned long long)t >> 32 ? (int)(t % n) : (int)((unsigned)t % (unsigned)n);
+}
+
 template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p) {
   griddep_launch_dependents();
@@ -70,6 +75,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   const long long taken = p.ring_pos[0], returned = p.ring_pos[1];
   const long long row_cap = (long long)p.W * page;
   auto pages_of = [&](int n) { return p.by_page(n) + (p.by_page(n) * page < n ? 1 : 0); };
+  const int ring_t = ring_start(taken, p.n_ring), ring_b = ring_start(returned, p.n_ring);
   __syncthreads();
   // each thread: `per` consecutive rows; 64-bit token sum, pages as need | back << 32
   const int per = (R + kMapThreads - 1) / kMapThreads;
@@ -174,10 +180,8 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   }
   if (p.cu)
     for (int r = me; r <= R; r += n_thr) p.cu[r] = bad ? 0 : tok[r];
-  const int ring_t = (int)(taken % p.n_ring);
   // per step of a thread: one new table entry, one returned page and kTok tokens, whose
   // bisections and look-ups are all under way before the first result is needed
-  const int ring_b = (int)(returned % p.n_ring);
   const int taken_n = bad ? 0 : (int)n_need, back_n = bad ? 0 : (int)n_back;
   const int pages_n = max(taken_n, back_n);
   long long i0 = me;  // tokens i0, i0 + n_thr, ..

@@ -390,12 +390,14 @@ extern "C" vkv_status vkv_page_select(const vkv_page_select_args* a, vkv_stream_
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int seqs = a->R * a->Hkv;
   if (a->W > a->topk) {
-    // steps per warp: about two rounds of the GPU's warps, whose rows end at different places
+    // steps per warp: one round of the GPU's warps, or rounds of 16 steps (rows end at different
+    // places; 32 rows of 16001 to 48000 tokens: 41.5 us with 4, 37.5 with 8, 35.2 with 16)
     const int step = kScoreStage / (4 * a->d);
     const long long row_steps = ((long long)a->W + step - 1) / step;
     const int warps = std::min(kScoreWarps, a->Hkv);
     p.head_groups = (a->Hkv + kScoreWarps - 1) / kScoreWarps;
-    p.score_steps = (int)std::min<long long>(8, std::max<long long>(1, seqs * row_steps / (2ll * 2 * kScoreWarps * n_sm)));
+    const long long round = 2ll * kScoreWarps * n_sm;
+    p.score_steps = (int)std::min<long long>(16, (seqs * row_steps + round - 1) / round);
     p.score_steps = (int)std::max<long long>(p.score_steps, (row_steps + 65534) / 65535);
     const dim3 grid((unsigned)(a->R * p.head_groups), (unsigned)((row_steps + p.score_steps - 1) / p.score_steps));
     const size_t smem = (size_t)warps * kScoreStages * kScoreStage;
