@@ -540,7 +540,7 @@ typedef enum {
  * VKV_DEVERR_NO_SPACE (too few free pages, or more tokens than max_tokens or than
  * W * page in a row) or VKV_DEVERR_BAD_OFFSETS (a length below -1 or above W * page, ring
  * positions that do not describe 0..n_ring free pages, or pages returned beyond n_ring).
- * kv_len_out may be kv_len and ring_pos_out may be ring_pos.
+ * kv_len_out may be kv_len and ring_pos_out may be ring_pos; other arrays do not overlap.
  */
 typedef struct {
   int32_t R;               /* rows, 1..VKV_PAGE_MAX_ROWS                              */
@@ -636,7 +636,9 @@ vkv_status vkv_page_select(const vkv_page_select_args* args, vkv_stream_t stream
  * (sink tokens + local window); when sel is given, only those of the selected pages.
  *   s_t = scale * <q, k_t>,  o = sum_t softmax(s)_t v_t,  lse = ln sum_t exp(s_t),
  * with k_t = k_scale[head] * stored for a VKV_E4M3 cache, values alike.  What the pages hold
- * beyond the visible tokens (any bits) has no effect.  A row with no visible token gives
+ * beyond the visible tokens (any bits) has no effect.  A visible infinite value makes its
+ * channel of o infinite or NaN.  o and lse overlap none of the inputs.  A row with no
+ * visible token gives
  * o = 0 and lse = -inf; the outputs of a row with kv_len = -1 are left as they were.  A
  * length below -1 or above W * page raises VKV_DEVERR_BAD_OFFSETS and its row's outputs
  * are left as they were; a page number outside [0, n_pages) or a selected page outside

@@ -5,6 +5,7 @@
 // here: each function checks its tensors, fills the C struct and calls the entry point whose
 // address it is given.  A refused argument is a ValueError; the C status is returned.
 #include <Python.h>
+#include <ATen/MemoryOverlap.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -76,15 +77,24 @@ int32_t dtype_of(const at::Tensor& x, const char* what) {
   }
 }
 
+// The stride of an axis as the entry points check it: that of an axis of one is never used, and
+// torch leaves there what it likes.
+int64_t step(const at::Tensor& x, int64_t axis) { return x.size(axis) > 1 ? x.stride(axis) : 0; }
+
+// For a tensor that is written: two of its elements must not be one (an expanded tensor).
+void no_overlap(const at::Tensor& x, const char* what) {
+  if (at::has_internal_overlap(x) == at::MemOverlap::Yes) throw Refusal{std::string(what) + " overlaps itself"};
+}
+
 // [.., .., d] with contiguous d: outer and inner stride of a 3-d tensor
 vkv_tensor rows3(const at::Tensor& x, const char* what, int dev, bool outer_is_row) {
   if (x.dim() != 3 || !x.is_cuda() || x.get_device() != dev || x.stride(2) != 1)
     throw Refusal{std::string(what) + " must be a 3-d tensor with contiguous last axis" + place(dev)};
   vkv_tensor t;
   t.ptr = x.data_ptr();
-  t.sb = outer_is_row ? x.stride(0) : 0;
-  t.st = outer_is_row ? 0 : x.stride(0);
-  t.sh = x.stride(1);
+  t.sb = outer_is_row ? step(x, 0) : 0;
+  t.st = outer_is_row ? 0 : step(x, 0);
+  t.sh = step(x, 1);
   return t;
 }
 
@@ -118,8 +128,8 @@ Cache cache_of(PyObject* ko, PyObject* vo, int dev) {
   c.Hkv = size_of(k.size(2), "Hkv");
   c.d = size_of(k.size(3), "d");
   c.dtype = dtype_of(k, "the cache");
-  c.k = {k.data_ptr(), k.stride(0), k.stride(1), k.stride(2)};
-  c.v = {v.data_ptr(), v.stride(0), v.stride(1), v.stride(2)};
+  c.k = {k.data_ptr(), step(k, 0), step(k, 1), step(k, 2)};
+  c.v = {v.data_ptr(), step(v, 0), step(v, 1), step(v, 2)};
   return c;
 }
 
@@ -192,6 +202,7 @@ PyObject* page_map(PyObject*, PyObject* const* x, Py_ssize_t n) {
     a.ring = vec<int32_t>(x[5], "ring", at::kInt, {n_ring}, dev);
     a.ring_pos = vec<int64_t>(x[6], "ring_pos", at::kLong, {2}, dev);
     a.kv_len_out = vec<int32_t>(x[9], "out['kv_len']", at::kInt, {R}, dev);
+    if (a.kv_len_out == a.new_len && R > 0) throw Refusal{"out['kv_len'] must not be new_len"};
     a.ring_pos_out = vec<int64_t>(x[10], "out['ring']", at::kLong, {2}, dev);
     a.slot = vec<int64_t>(x[11], "out['slot']", at::kLong, {a.max_tokens}, dev);
     a.row = vec<int32_t>(x[12], "out['row']", at::kInt, {a.max_tokens}, dev, true);
@@ -214,6 +225,9 @@ PyObject* page_append(PyObject*, PyObject* const* x, Py_ssize_t n) {
     vkv_page_append_args a{};
     a.T = size_of(kn.size(0), "k_new");
     a.Hkv = c.Hkv, a.d = c.d, a.page = c.page, a.n_pages = c.n_pages;
+    no_overlap(tensor(x[5], "k_pages"), "k_pages");
+    no_overlap(tensor(x[6], "v_pages"), "v_pages");
+    if (c.k.ptr && c.k.ptr == c.v.ptr) throw Refusal{"k_pages and v_pages must not be one tensor"};
     a.x_dtype = dtype_of(kn, "k_new");
     a.kv_dtype = c.dtype;
     a.k_new = rows3(kn, "k_new", dev, false);
@@ -261,6 +275,9 @@ PyObject* page_attn(PyObject*, PyObject* const* x, Py_ssize_t n) {
     const Cache c = cache_of(x[3], x[4], dev);
     if (q.dim() != 3 || q.size(2) != c.d) throw Refusal{"q must be [R, H, d], d as in the cache"};
     if (o.sizes() != q.sizes() || o.scalar_type() != q.scalar_type()) throw Refusal{"o must have the shape and type of q"};
+    // a row's queries may be read again after some of its outputs are written
+    if (q.numel() && o.data_ptr() == q.data_ptr()) throw Refusal{"o must not be q"};
+    no_overlap(o, "o");
     vkv_page_attn_args a{};
     const int64_t R = q.size(0), H = q.size(1);
     a.R = size_of(R, "q"), a.H = size_of(H, "q");

@@ -576,6 +576,48 @@ def test_attn_workspace_argument():
         attn_call(c, workspace=ws[:128])
 
 
+def test_strides_of_axes_of_one_do_not_count():
+    """One row, one head, one page, one token: torch leaves any stride on such an axis."""
+    d, P = 64, 16
+    c = attn_case(R=1, H=1, Hkv=1, d=d, P=P, lens=[13], poison=False, seed=3)
+    want = attn_call(c)
+
+    def odd(x, *strides):
+        return x.as_strided(x.shape, strides)
+
+    q = odd(c["q"], 3, 5, 1)
+    o, lse = odd(torch.empty_like(c["q"]), 7, 1, 1), torch.empty((1, 1), device=DEV)
+    k, v = (odd(c[n], P * d, d, 3, 1) for n in ("k", "v"))
+    got = attn_call({**c, "q": q, "k": k, "v": v}, out=(o, lse))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    bar = torch.randn((c["k"].shape[0], 1, d), device=DEV)
+    sel = vkv.page_select(q, bar, c["table"], i32([13]), P, 1)
+    assert sel.tolist() == [[[0]]]
+    x = odd(torch.randn((1, 1, d), device=DEV).to(torch.bfloat16), 1, 3, 1)
+    one_k, one_v = (odd(torch.zeros((1, 1, 1, d), dtype=torch.bfloat16, device=DEV), 5, 3, 7, 1) for _ in range(2))
+    vkv.page_append(x, x, torch.zeros(1, dtype=torch.int64, device=DEV), one_k, one_v)
+    assert torch.equal(bits(one_k).flatten(), bits(x).flatten()) and torch.equal(bits(one_v).flatten(), bits(x).flatten())
+
+
+def test_outputs_that_overlap_are_refused():
+    c = attn_case(R=2, H=4, Hkv=2, d=64, P=16, lens=[20, 5], poison=False)
+    lse = torch.empty((2, 4), device=DEV)
+    with pytest.raises(ValueError, match="o must not be q"):
+        attn_call(c, out=(c["q"], lse))
+    with pytest.raises(ValueError, match="overlaps itself"):
+        attn_call(c, out=(torch.empty_like(c["q"][:1]).expand(2, 4, 64), lse))
+    x, slot = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    with pytest.raises(ValueError, match="must not be one tensor"):
+        vkv.page_append(x, x, slot, c["k"], c["k"])
+    with pytest.raises(ValueError, match="overlaps itself"):
+        vkv.page_append(x, x, slot, c["k"][:1].expand(c["k"].shape), c["v"])
+    n = i32([0, 0])
+    out = {"kv_len": n, "ring": torch.empty(2, dtype=torch.int64, device=DEV),
+           "slot": torch.empty(4, dtype=torch.int64, device=DEV)}
+    with pytest.raises(ValueError, match="must not be new_len"):
+        vkv.page_map(i32([0, 0]), n, i32([[0], [0]]), i32([0]), torch.zeros(2, dtype=torch.int64, device=DEV), 16, 4, out=out)
+
+
 # ---------------------------------------------------------------------------------------------
 # a run of them together
 # ---------------------------------------------------------------------------------------------
