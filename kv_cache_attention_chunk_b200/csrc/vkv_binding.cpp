@@ -227,7 +227,6 @@ PyObject* page_append(PyObject*, PyObject* const* x, Py_ssize_t n) {
     a.Hkv = c.Hkv, a.d = c.d, a.page = c.page, a.n_pages = c.n_pages;
     no_overlap(tensor(x[5], "k_pages"), "k_pages");
     no_overlap(tensor(x[6], "v_pages"), "v_pages");
-    if (c.k.ptr && c.k.ptr == c.v.ptr) throw Refusal{"k_pages and v_pages must not be one tensor"};
     a.x_dtype = dtype_of(kn, "k_new");
     a.kv_dtype = c.dtype;
     a.k_new = rows3(kn, "k_new", dev, false);
