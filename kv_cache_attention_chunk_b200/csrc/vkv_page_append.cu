@@ -135,7 +135,6 @@ constexpr int kAppendRows = 4;
 
 template <int D, typename IN, bool E4M3>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
-  griddep_launch_dependents();
   griddep_wait();
   constexpr int CPR = D / 8;
   constexpr int OB = E4M3 ? 8 : 16;  // bytes of a stored chunk
@@ -167,6 +166,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     store_chunk<IN, E4M3>(p.k + pg * p.k_sb + off * p.k_st + h * p.k_sh + c * OB, kx[e], by_k, nullptr);
     store_chunk<IN, E4M3>(p.v + pg * p.v_sb + off * p.v_st + h * p.v_sh + c * OB, vx[e], by_v, nullptr);
   }
+  griddep_launch_dependents();
 }
 
 // With means: a warp takes the runs that start among `slab` (<= 32) consecutive tokens, for
@@ -186,7 +186,6 @@ __global__ void __launch_bounds__(kMeanWarps * 32, 5) append_mean_kernel(const A
   constexpr int GROUPS = 32 / CPR * (SPLIT ? kMeanWarps : 1);  // rows at a time
   constexpr int OB = E4M3 ? 8 : 16;
   __shared__ float part[SPLIT ? kMeanWarps : 1][D];
-  griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = SPLIT ? blockIdx.y : blockIdx.y * kMeanWarps + warp;
@@ -296,6 +295,7 @@ __global__ void __launch_bounds__(kMeanWarps * 32, 5) append_mean_kernel(const A
       dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
     }
   }
+  griddep_launch_dependents();
 }
 
 template <int D, typename IN, bool E4M3>

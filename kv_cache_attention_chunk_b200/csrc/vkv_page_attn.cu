@@ -8,8 +8,10 @@
 //
 // Work: the visible tokens of a (row, key head, chunk of up to 16 query heads) are a unit,
 // cut into tiles of TT tokens; all units' tiles form one line, which is dealt out to the
-// warps of a grid of two blocks per SM in equal contiguous shares.  So rows of any length
-// mix, one long row fills the GPU, and no host code needs the lengths.  Each warp streams
+// warps of a grid of two or three blocks per SM in equal contiguous shares.  So rows of any
+// length mix, one long row fills the GPU, and no host code needs the lengths.  Short calls are
+// latencies, and joins are the longest of them: there the line is made of blocks, whole ones
+// for each unit, so that no block has parts of two units to join one after the other.  Each warp streams
 // its own share through a private ring of cp.async stages (K and V of a tile, addresses from
 // the block table, masked tokens zero-filled); warps never wait for one another until the
 // end.  A unit within one warp's share is finished there.  A unit cut by shares leaves its
@@ -40,10 +42,17 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxBlocksPerSm = 3;
 constexpr int kMaxBlocks = kMaxBlocksPerSm * kMaxCtas;
 constexpr float kSlack = 4.f;  // log2: how far a score may exceed the running maximum
-// The least share of a warp: short shares spread a small call over more SMs but leave more
-// parts to join (one row of 1560 tokens 14.2 us with 2 tiles, 16.5 with 4; two rows of 64
-// selected pages of 64 tokens 41 and 35 us, selection included)
-constexpr int kMinTiles = 2, kMinTilesLong = 4, kLongUnit = 160;
+// The least share of a warp, tiles: a share of t tiles takes t times a tile's time and leaves
+// (tiles of the unit) / t parts to join, so the best t grows with the root of the unit's tiles
+// (one row of 131072 tokens, one head: 39 us with these factors, 54 with 4 tiles; 4 key heads of
+// 9097 tokens 23 and 27; one row of 1560 tokens 14 with 2 tiles, 16.5 with 4).  Chunks of 16 heads
+// have twice the joins per warp.
+constexpr int kMinTiles = 2;
+constexpr float kShareRoot[2] = {0.045f, 0.14f};  // for chunks of 8 and of 16 heads
+// Calls of at most this many tiles per warp give each unit whole blocks (two rows of 520 tokens,
+// 8 key heads of 64 channels: 9.8 us, on the line 16.3; one row of 1560 tokens 12.0 and 14.1; above
+// it equal shares count for more)
+constexpr int kWholeMost = 8;
 
 struct PageAttnParams {
   int R, H, Hkv, G, page, n_pages, W, sink, window, topk;
@@ -217,6 +226,12 @@ struct Shares {
   }
 };
 
+// What the joins need to know of the line, the same in all of a block's warps.
+struct Line {
+  Shares sh;
+  int pair, unit_b0, unit_nb;  // unit_nb > 0: whole blocks per unit, of this one its first block and its blocks
+};
+
 template <int D>
 struct Vec;
 template <>
@@ -251,18 +266,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   extern __shared__ __align__(256) char smem[];
   __shared__ int4 meta[kWarps][Z::S];  // of a stage: token mask, row, key head << 16 | chunk of query heads, flags
   __shared__ Part parts[2 * kWarps];
+  __shared__ Line line;  // (not in registers: it is not needed while the tiles are streamed)
   __shared__ int4 pending[4];
   __shared__ int s_last[4];
 
-  griddep_launch_dependents();
   griddep_wait();  // launched ahead of the end of the stream's last kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
-  // the line's heads: key heads, or pairs of them, of which an even and an odd warp take one each
-  const int heads = p.Hkv >> p.pair, U = heads * p.n_chunks, sub = warp & p.pair;
-  const int kw = kWarps >> p.pair, kw_log = 2 - p.pair;  // the block's shares
-  static_assert(kWarps == 4, "kw_log");
-
   // a row's visible tokens: x in [0, n) is token x (x < lo) or x + gap, or token x % page of
   // selected page x / page
   auto row_len = [&](int r) {
@@ -297,24 +307,71 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     mine += t;
     longest = max(longest, t);
   }
+  long long all = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+  if (all == 0) return;
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  const int least = max(kMinTiles, (int)sqrtf(kShareRoot[NT - 1] * (float)longest));
+  // Small calls: whole blocks per unit (of shares of `tb` / kWarps tiles at most), if the grid has
+  // that many blocks
+  int tb = 0, nb = 0;  // tiles of a block, or 0; blocks of the lane's rows, per unit
+  {
+    const int units = p.Hkv * p.n_chunks;
+    const long long even = quotient(all * units + gridDim.x * kWarps - 1, (long long)gridDim.x * kWarps);
+    if (even <= kWholeMost && (long long)p.R * units <= 4 * kMaxBlocks) {
+      const int s0 = max(least, (int)even);
+#pragma unroll 1
+      for (int s = s0; s <= s0 + 1 + s0 / 4; ++s) {
+        nb = 0;
+        if (per == 1) nb = ((int)mine + s * kWarps - 1) / (s * kWarps);
+        else
+          for (int r = r0; r < r1; ++r) nb += (row_tiles(row_len(r)) + s * kWarps - 1) / (s * kWarps);
+        if (__reduce_add_sync(0xFFFFFFFFu, nb) * units <= (int)gridDim.x) {
+          tb = s * kWarps;
+          break;
+        }
+      }
+    }
+  }
+  // the line's heads: key heads, or pairs of them, of which an even and an odd warp take one each
+  const int pair = tb ? 0 : p.pair;
+  const int heads = p.Hkv >> pair, U = heads * p.n_chunks, sub = warp & pair;
+  const int kw = kWarps >> pair;  // the block's shares
+  // a row's part of the line, for each of its units: tiles, or blocks
+  auto extent = [&](int len) {
+    const int t = row_tiles(len);
+    return tb ? (t + tb - 1) / tb : t;
+  };
+  if (tb) mine = nb;
   long long before = warp_scan(mine, lane);
   const long long total = __shfl_sync(0xFFFFFFFFu, before, 31) * U;
   before -= mine;
-  if (total == 0) return;
-  const int least = __reduce_max_sync(0xFFFFFFFFu, longest) < kLongUnit ? kMinTiles : kMinTilesLong;
-  const long long n_share = min((long long)gridDim.x * kw, quotient(total + least - 1, least));
-  if ((long long)blockIdx.x * kw >= n_share) return;
   Shares sh;
-  sh.q = quotient(total, n_share);
-  sh.rem = total - sh.q * n_share;
-  sh.n = (int)n_share;
-  const long long my_w = (long long)blockIdx.x * kw + (warp >> p.pair);
+  sh.q = sh.rem = sh.n = 0;
+  int count = 0;                 // tiles of the warp
+  long long line0 = blockIdx.x;  // where on the line the warp, or block, begins
+  if (tb) {
+    if (line0 >= total) return;
+  } else {
+    const long long n_share = min((long long)gridDim.x * kw, quotient(total + least - 1, least));
+    if (line0 * kw >= n_share) return;
+    sh.q = quotient(total, n_share);
+    sh.rem = total - sh.q * n_share;
+    sh.n = (int)n_share;
+    const long long my_w = line0 * kw + (warp >> pair);
+    count = my_w < n_share ? (int)(sh.q + (my_w < sh.rem ? 1 : 0)) : 0;
+    line0 = sh.begin(my_w);
+    if (lane == 0) {
+      line.sh = sh;
+      line.pair = pair;
+      line.unit_nb = 0;
+    }
+  }
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * Z::WARP);
   if (lane < 2) parts[2 * warp + lane].te = 0;
-  int count = my_w < n_share ? (int)(sh.q + (my_w < sh.rem ? 1 : 0)) : 0;
-  if (count > 0) {
-    const long long line0 = sh.begin(my_w);
-    // the row of tile line0: the lane whose rows hold it, then (long batches) the row among them
+  if (tb || count > 0) {
+    // the row there: the lane whose rows hold it, then (long batches) the row among them
     const int src = __ffs(__ballot_sync(0xFFFFFFFFu, line0 < (before + mine) * U)) - 1;
     long long row0 = __shfl_sync(0xFFFFFFFFu, before, src) * U;
     int cr = src * per;
@@ -323,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     } else {
       for (; cr < p.R; cr += 32) {
         const int l = cr + lane < p.R ? row_len(cr + lane) : -1;
-        const long long t = row_tiles(l), a = warp_scan(t, lane);
+        const long long t = extent(l), a = warp_scan(t, lane);
         const unsigned b = __ballot_sync(0xFFFFFFFFu, line0 < row0 + a * U);
         if (b) {
           const int x = __ffs(b) - 1;
@@ -337,8 +394,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     }
     int lo, gap, n_vis = visible(len, lo, gap);
     int tiles = row_tiles(len);
-    const int cu = (int)quotient(line0 - row0, tiles);
-    int ct = (int)(line0 - row0 - (long long)cu * tiles);
+    const int ext = extent(len), cu = (int)quotient(line0 - row0, ext);
+    int ct = (int)(line0 - row0 - (long long)cu * ext);
+    if (tb) {  // the unit's tiles in equal shares to the warps of its blocks
+      if (lane == 0) {
+        line.pair = 0;
+        line.unit_b0 = blockIdx.x - ct;
+        line.unit_nb = ext;
+      }
+      const int q = tiles / (ext * kWarps), rem = tiles - q * ext * kWarps, w = ct * kWarps + warp;
+      count = q + (w < rem ? 1 : 0);
+      ct = w * q + min(w, rem);
+    }
     int chead = cu / p.n_chunks, chunk = cu - chead * p.n_chunks;
     const int ct0 = ct;
     // ---- cursor: the next tile to look up
@@ -351,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     // flags: 1 the share's piece of a unit begins, 2 it ends, 4 the unit begins, 8 the unit ends
     auto lookup = [&]() {
       nx_r = cr;
-      const int head = (chead << p.pair) + sub;
+      const int head = (chead << pair) + sub;
       nx_hc = head << 16 | chunk;
       nx_flags = (first || ct == 0 ? 1 : 0) | (todo == 1 || ct == tiles - 1 ? 2 : 0) | (ct == 0 ? 4 : 0) |
                  (ct == tiles - 1 ? 8 : 0);
@@ -724,14 +791,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
           }
           if (lane == 0) {
             const int tl = row_tiles(row_len(r));
-            const int tb = is_first ? ct0 : 0;
+            const int t0 = is_first ? ct0 : 0;
             Part& pt = parts[slot];
             pt.r = r;
             pt.u = h * p.n_chunks + (mt.z & 0xFFFF);
-            pt.tb = tb;
-            pt.te = tb + piece_n;
+            pt.tb = t0;
+            pt.te = t0 + piece_n;
             pt.tiles = tl;
-            pt.unit0 = line0 + piece_t0 - tb;
+            pt.unit0 = line0 + piece_t0 - t0;
           }
         }
       }
@@ -741,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   }
   __syncthreads();
 
+  griddep_launch_dependents();
   // ---- join the block's parts; units that go on in other blocks meet in the workspace
   auto part_o = [&](int i) {
     return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * Z::WARP)
@@ -754,14 +822,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
       p.lse[(size_t)r * p.H + head] =
           sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - kShift + log2f(sum)) * 0.69314718055994531f;
   };
+  const int jp = line.pair;
   // lane j holds part j (2 w: warp w's first, 2 w + 1: its last); parts of one unit are neighbours
   const int my_part = lane & (2 * kWarps - 1);
   const Part mp = parts[my_part];
   unsigned todo = __ballot_sync(0xFFFFFFFFu, lane < 2 * kWarps && mp.te > 0);
   int my_b0 = 0, my_n = 0, n_pending = 0;
   if (todo >> my_part & 1u) {
-    my_b0 = sh.of(mp.unit0) >> kw_log;
-    my_n = (sh.of(mp.unit0 + mp.tiles - 1) >> kw_log) - my_b0 + 1;
+    static_assert(kWarps == 4, "2 - pair: the logarithm of the block's shares");
+    my_b0 = line.unit_nb ? line.unit_b0 : line.sh.of(mp.unit0) >> (2 - jp);
+    my_n = line.unit_nb ? line.unit_nb : (line.sh.of(mp.unit0 + mp.tiles - 1) >> (2 - jp)) - my_b0 + 1;
   }
 #pragma unroll 1
   while (todo) {
@@ -769,12 +839,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     const int r = __shfl_sync(0xFFFFFFFFu, mp.r, i), u = __shfl_sync(0xFFFFFFFFu, mp.u, i);
     const unsigned grp = __ballot_sync(0xFFFFFFFFu, mp.r == r && mp.u == u) & todo;
     todo &= ~grp;
-    const int tb = __shfl_sync(0xFFFFFFFFu, mp.tb, i), tiles = __shfl_sync(0xFFFFFFFFu, mp.tiles, i);
+    const int t0 = __shfl_sync(0xFFFFFFFFu, mp.tb, i), tiles = __shfl_sync(0xFFFFFFFFu, mp.tiles, i);
     const int te = __shfl_sync(0xFFFFFFFFu, mp.te, 31 - __clz(grp));
     const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
-    const bool whole = tb == 0 && te == tiles;
+    const bool whole = t0 == 0 && te == tiles;
     const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
-    const size_t ws = (((size_t)(2 * blockIdx.x + (tb == 0 ? 1 : 0)) << p.pair) + (h & p.pair)) * hcw;
+    const size_t ws = (((size_t)(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) << jp) + (h & jp)) * hcw;
     // the warps' parts of this unit (at most one each)
     const float* src[kWarps];
 #pragma unroll
@@ -813,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     if (!whole) {
       const int b0 = __shfl_sync(0xFFFFFFFFu, my_b0, i), n = __shfl_sync(0xFFFFFFFFu, my_n, i);
       // row, key head << 16 | chunk, first block << pair | the head's place in its pair, blocks
-      if (tid == 0) pending[n_pending] = make_int4(r, h << 16 | (u - h * p.n_chunks), b0 << p.pair | (h & p.pair), n);
+      if (tid == 0) pending[n_pending] = make_int4(r, h << 16 | (u - h * p.n_chunks), b0 << jp | (h & jp), n);
       ++n_pending;  // two per head at most: what began in an earlier block, and what goes on in a later one
     }
   }
@@ -840,8 +910,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
       V4 x[HW];
       // part 0 lies among its block's lasts, the others among their blocks' firsts
       constexpr int kBatch = 8;  // loads in flight per head
-      const int b0 = first >> p.pair, stride = (2 * hcw) << p.pair;
-      const size_t row1 = (size_t)(b0 + 1) * stride + (first & p.pair) * hcw, row0 = row1 - (hcw << p.pair);
+      const int b0 = first >> jp, stride = (2 * hcw) << jp;
+      const size_t row1 = (size_t)(b0 + 1) * stride + (first & jp) * hcw, row0 = row1 - (hcw << jp);
       auto at = [&](int j, int hd) { return (j == 0 ? row0 : row1 + (size_t)(j - 1) * stride) + hd; };
       V4 y[HW][kBatch];
       auto load = [&](int j0) {
@@ -1012,8 +1082,8 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   const long long most = a->sel ? std::min<long long>((long long)a->topk * a->page, (long long)a->W * a->page)
                          : a->window > 0 ? std::min<long long>((long long)a->sink + a->window, (long long)a->W * a->page)
                                          : (long long)a->W * a->page;
-  const long long tiles = ((most + tt - 1) / tt) * a->R * a->Hkv * p.n_chunks;
-  const int blocks = (int)std::min<long long>(all, (tiles + kMinTiles * kWarps - 1) / (kMinTiles * kWarps));
+  const long long row_blocks = (std::max<long long>(1, (most + tt - 1) / tt) + kMinTiles * kWarps - 1) / (kMinTiles * kWarps);
+  const int blocks = (int)std::min<long long>(all, row_blocks * a->R * a->Hkv * p.n_chunks);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t rc = a->d == 128 ? launch_d<128>(p, a->q_dtype, a->kv_dtype, blocks, n_sm, dev, st)
                                      : launch_d<64>(p, a->q_dtype, a->kv_dtype, blocks, n_sm, dev, st);

@@ -59,7 +59,6 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(const S
   constexpr int PASSES = kScoreStage / (4 * 4 * D);  // pages of a lane group per stage
   constexpr int STEP = 4 * PASSES;                   // pages per step
   extern __shared__ __align__(16) char ring[];
-  griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7;
   const int r = blockIdx.x / p.head_groups, g = (blockIdx.x - r * p.head_groups) * kScoreWarps + warp;
@@ -153,6 +152,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(const S
       for (int e = 0; e < PASSES; ++e) pg[s][e] = pg[s + 1][e];
     stage = stage + 1 == kScoreStages ? 0 : stage + 1;
   }
+  griddep_launch_dependents();
 }
 
 constexpr int kPickThreads = 256;
@@ -194,7 +194,6 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
   __shared__ int cand_page[kCand];
   __shared__ int s_bin, s_above, s_in, s_n, s_page;
   __shared__ unsigned long long s_key;
-  griddep_launch_dependents();
   griddep_wait();  // the scores
   const int r = blockIdx.x / p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -227,6 +226,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
       for (int j = a; j < b; ++j) f(j, keys[j]);
     }
   };
+  griddep_launch_dependents();
   for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
   if (tid == 0) s_n = 0;
   // the finite scores' range
