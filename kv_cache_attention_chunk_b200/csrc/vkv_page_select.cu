@@ -51,8 +51,9 @@ constexpr int kScoreStage = 4096;  // bytes of means that a warp fetches at a ti
 // by side), 8 lanes per page.  grid: x = row and head group, y = chunks of the table's width
 // (p.score_steps steps of a warp).  HBM-bound (4 d bytes per page and key head): each lane
 // streams the pieces of the means that it will use itself through a private cp.async ring, so
-// that 128 KB per SM are in flight with no registers held and no barriers.  Length, table
-// and queries are asked for together.  The fp64 products hide behind the loads.
+// that 128 KB per SM are in flight with no registers held and no barriers.  Length and table are
+// asked for together, the queries while the first means are on their way.  The fp64 products
+// hide behind the loads.
 template <int D, typename T>
 __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(const SelParams p) {
   constexpr int PC = D / 32;                         // 16-byte pieces of a lane per page: 4 channels of each 32
@@ -70,22 +71,6 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(const S
   int ahead[PASSES];                // table entries of the next step to fetch
 #pragma unroll
   for (int e = 0; e < PASSES; ++e) ahead[e] = jl + e * 4 < p.W ? tab[jl + e * 4] : -1;
-  const T* q = reinterpret_cast<const T*>(p.q) + r * p.q_sb + (long long)g * p.G * p.q_sh + sub * 4;
-  double qr[4 * PC];  // the group's summed queries, at the lane's channels
-#pragma unroll
-  for (int i = 0; i < 4 * PC; ++i) qr[i] = 0.0;
-#pragma unroll 2
-  for (int i = 0; i < p.G; ++i) {
-    uint2 x[PC];
-#pragma unroll
-    for (int c = 0; c < PC; ++c) x[c] = *reinterpret_cast<const uint2*>(q + i * p.q_sh + c * 32);
-#pragma unroll
-    for (int c = 0; c < PC; ++c) {
-      const T* e = reinterpret_cast<const T*>(&x[c]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) qr[4 * c + k] += (double)(float)e[k];
-    }
-  }
   const int len = page_row_len(raw, p.W, p.page, p.err);
   const int n = len <= 0 ? 0 : p.by_page(len) + (p.by_page(len) * p.page < len ? 1 : 0);
   if (j0 >= n || n <= p.topk) return;  // all of a short row's pages are kept: no ranking
@@ -114,6 +99,22 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(const S
   };
 #pragma unroll
   for (int s = 0; s < kScoreStages - 1; ++s) fetch(s, s, pg[s]);
+  const T* q = reinterpret_cast<const T*>(p.q) + r * p.q_sb + (long long)g * p.G * p.q_sh + sub * 4;
+  double qr[4 * PC];  // the group's summed queries, at the lane's channels
+#pragma unroll
+  for (int i = 0; i < 4 * PC; ++i) qr[i] = 0.0;
+#pragma unroll 4
+  for (int i = 0; i < p.G; ++i) {
+    uint2 x[PC];
+#pragma unroll
+    for (int c = 0; c < PC; ++c) x[c] = *reinterpret_cast<const uint2*>(q + i * p.q_sh + c * 32);
+#pragma unroll
+    for (int c = 0; c < PC; ++c) {
+      const T* e = reinterpret_cast<const T*>(&x[c]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) qr[4 * c + k] += (double)(float)e[k];
+    }
+  }
   unsigned long long* out = p.keys + ((size_t)r * p.Hkv + g) * p.W;
   int stage = 0;
 #pragma unroll 1
@@ -155,48 +156,63 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(const S
   griddep_launch_dependents();
 }
 
-constexpr int kPickThreads = 256;
+constexpr int kPickThreads = 1024;
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kHeld = 8;
 constexpr int kCand = 512;  // keys of one bin that are ranked by comparing each with each
+static_assert(kPickWarps == 32 && kBins == 2 * kPickThreads, "a lane per warp; two bins per thread");
 
 // Inclusive sum over the block, in thread order; `total` is the block's sum.
-__device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ int warp_incl(int x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
     if (lane >= o) x += y;
   }
+  return x;
+}
+__device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  x = warp_incl(x, lane);
   __syncthreads();  // the last call's sums have been read
   if (lane == 31) warp_sum[warp] = x;
   __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kPickWarps; ++w) {
-    if (w < warp) x += warp_sum[w];
-    total += warp_sum[w];
-  }
-  return x;
+  const int w = warp_incl(warp_sum[lane], lane);
+  total = __shfl_sync(0xFFFFFFFFu, w, 31);
+  const int before = __shfl_sync(0xFFFFFFFFu, w, (warp + 31) & 31);
+  return warp ? x + before : x;
 }
+
+// A float's order-preserving image and back.
+__device__ __forceinline__ uint32_t order_of(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t u) { return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
 
 // One block per (row, key head): the topk largest keys, of equal ones the lowest pages.
 // The scores are dealt to bins of equal width between the least and the largest (a page's
 // bin never decreases with its key, whatever the rounding); the bin that holds the topk-th
 // key has few keys as a rule, and these are ranked one against the other.  Should it hold
 // many (equal scores, outliers), a radix selection, 8 bits a pass, finds the key instead.
+//
+// Bound: latency, of the code's own fetch too (it runs once).  So many threads have few pages
+// each: HELD (of up to 1024 HELD table columns) are kept in registers with their bins, 0 reads
+// the keys again in every step.  2000 pages: 7.8 us with 256 threads of 8 pages.
+template <int HELD>
 __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams p) {
   __shared__ int hist[kBins];
   __shared__ int warp_sum[kPickWarps];
-  __shared__ float warp_lo[kPickWarps], warp_hi[kPickWarps];
+  __shared__ uint32_t warp_lo[kPickWarps], warp_hi[kPickWarps];
   __shared__ unsigned long long cand_key[kCand];
   __shared__ int cand_page[kCand];
   __shared__ int s_bin, s_above, s_in, s_n, s_page;
   __shared__ unsigned long long s_key;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  reinterpret_cast<int2*>(hist)[tid] = make_int2(0, 0);
+  if (tid == 0) s_n = 0;
   griddep_wait();  // the scores
   const int r = blockIdx.x / p.Hkv;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int raw = p.kv_len[r];
   const int len = (raw >= -1 && (long long)raw <= (long long)p.W * p.page) ? raw : 0;
   const int n = len <= 0 ? 0 : p.by_page(len) + (p.by_page(len) * p.page < len ? 1 : 0);
@@ -209,83 +225,88 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
     return;
   }
   const unsigned long long* keys = p.keys + (size_t)blockIdx.x * p.W;
-  // thread t has the t-th run of pages, up to kHeld a thread in registers
-  const int per = (n + kPickThreads - 1) / kPickThreads, a = min(n, tid * per), b = min(n, a + per);
-  const bool held = per <= kHeld;
-  unsigned long long own[kHeld];
-  if (held) {
+  // thread t has the t-th run of pages
+  const int per = HELD ? HELD : (n - 1) / kPickThreads + 1;
+  const int a = (int)min((long long)n, (long long)tid * per), b = min(n - a, per) + a;
+  constexpr int N = HELD ? HELD : 1;
+  unsigned long long own[N];
+  float value[N];  // then the bin
+  int own_bin[N];
+  if (HELD) {
 #pragma unroll
-    for (int e = 0; e < kHeld; ++e) own[e] = a + e < b ? keys[a + e] : 0ull;
+    for (int e = 0; e < N; ++e) own[e] = a + e < b ? keys[a + e] : 0ull;
+#pragma unroll
+    for (int e = 0; e < N; ++e) value[e] = (float)key_value(own[e]);
   }
-  auto each = [&](auto&& f) {  // f(page, key) for the thread's pages
-    if (held) {
-#pragma unroll
-      for (int e = 0; e < kHeld; ++e)
-        if (a + e < b) f(a + e, own[e]);
-    } else {
-      for (int j = a; j < b; ++j) f(j, keys[j]);
+  // the finite scores' range
+  uint32_t lo_u = 0xFFFFFFFFu, hi_u = 0u;
+  auto widen = [&](unsigned long long k, float f) {
+    if (k != 0ull && k != ~0ull && fabsf(f) < INFINITY) {
+      lo_u = min(lo_u, order_of(f));
+      hi_u = max(hi_u, order_of(f));
     }
   };
-  griddep_launch_dependents();
-  for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
-  if (tid == 0) s_n = 0;
-  // the finite scores' range
-  float lo = INFINITY, hi = -INFINITY;
-  each([&](int, unsigned long long k) {
-    const float f = (float)key_value(k);
-    if (k != 0ull && k != ~0ull && fabsf(f) < INFINITY) {
-      lo = fminf(lo, f);
-      hi = fmaxf(hi, f);
-    }
-  });
+  if (HELD) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    for (int e = 0; e < N; ++e) widen(own[e], value[e]);
+  } else {
+    for (int j = a; j < b; ++j) widen(keys[j], (float)key_value(keys[j]));
   }
+  lo_u = __reduce_min_sync(0xFFFFFFFFu, lo_u);
+  hi_u = __reduce_max_sync(0xFFFFFFFFu, hi_u);
   if (lane == 0) {
-    warp_lo[warp] = lo;
-    warp_hi[warp] = hi;
+    warp_lo[warp] = lo_u;
+    warp_hi[warp] = hi_u;
   }
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kPickWarps; ++w) {
-    lo = fminf(lo, warp_lo[w]);
-    hi = fmaxf(hi, warp_hi[w]);
-  }
-  const float scale = hi > lo ? (float)(kBins - 3) / (hi - lo) : 0.f;
-  auto bin_of = [&](unsigned long long k) {
+  griddep_launch_dependents();
+  lo_u = __reduce_min_sync(0xFFFFFFFFu, warp_lo[lane]);
+  hi_u = __reduce_max_sync(0xFFFFFFFFu, warp_hi[lane]);
+  const float lo = order_value(lo_u), scale = hi_u > lo_u ? (float)(kBins - 3) / (order_value(hi_u) - lo) : 0.f;
+  auto bin_at = [&](unsigned long long k, float f) {
     if (k == 0ull) return 0;
     if (k == ~0ull) return kBins - 1;
-    return 1 + max(0, min(kBins - 3, __float2int_rd(((float)key_value(k) - lo) * scale)));
+    return 1 + max(0, min(kBins - 3, __float2int_rd((f - lo) * scale)));
   };
-  each([&](int, unsigned long long k) { atomicAdd(&hist[bin_of(k)], 1); });
-  __syncthreads();
-  {  // the bin of the topk-th key: thread t scans bins from the top
-    constexpr int B = kBins / kPickThreads;
-    int c[B], sum = 0, total;
+  if (HELD) {
 #pragma unroll
-    for (int e = 0; e < B; ++e) sum += c[e] = hist[kBins - 1 - (tid * B + e)];
-    int above = block_scan(sum, warp_sum, total) - sum;
+    for (int e = 0; e < N; ++e) own_bin[e] = a + e < b ? bin_at(own[e], value[e]) : -1;
+  }
+  auto each = [&](auto&& f) {  // f(page, key, bin) for the thread's pages
+    if (HELD) {
 #pragma unroll
-    for (int e = 0; e < B; ++e) {
-      if (above < p.topk && p.topk <= above + c[e]) {
-        s_bin = kBins - 1 - (tid * B + e);
-        s_above = above;
-        s_in = c[e];
+      for (int e = 0; e < N; ++e)
+        if (a + e < b) f(a + e, own[e], own_bin[e]);
+    } else {
+#pragma unroll 1
+      for (int j = a; j < b; ++j) {
+        const unsigned long long k = keys[j];
+        f(j, k, bin_at(k, (float)key_value(k)));
       }
-      above += c[e];
+    }
+  };
+  each([&](int, unsigned long long, int at) { atomicAdd(&hist[at], 1); });
+  __syncthreads();
+  {  // the bin of the topk-th key: thread t has bins 2 t and 2 t + 1 from the top
+    int total;
+    const int2 c = reinterpret_cast<const int2*>(hist)[kPickThreads - 1 - tid];
+    const int above = block_scan(c.x + c.y, warp_sum, total) - (c.x + c.y);
+    const bool up = p.topk <= above + c.y;
+    if (above < p.topk && p.topk <= above + c.x + c.y) {
+      s_bin = kBins - 1 - 2 * tid - (up ? 0 : 1);
+      s_above = above + (up ? 0 : c.y);
+      s_in = up ? c.y : c.x;
     }
   }
   __syncthreads();
   const int bin = s_bin, n_in = s_in;
   int need = p.topk - s_above;  // keys of the bin to take: at least one, at most n_in
   if (n_in <= kCand) {
-    each([&](int j, unsigned long long k) {
-      if (bin_of(k) == bin) {
-        const int at = atomicAdd(&s_n, 1);
-        cand_key[at] = k;
-        cand_page[at] = j;
+    each([&](int j, unsigned long long k, int at) {
+      if (at == bin) {
+        const int i = atomicAdd(&s_n, 1);
+        cand_key[i] = k;
+        cand_page[i] = j;
       }
     });
     __syncthreads();
@@ -304,14 +325,14 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
 #pragma unroll 1
     for (int shift = 56; shift >= 0; shift -= 8) {
       __syncthreads();
-      hist[tid] = 0;
+      if (tid < 256) hist[tid] = 0;
       __syncthreads();
-      each([&](int, unsigned long long k) {
-        if ((k & mask) == thr && bin_of(k) == bin) atomicAdd(&hist[(int)(k >> shift) & 255], 1);
+      each([&](int, unsigned long long k, int at) {
+        if ((k & mask) == thr && at == bin) atomicAdd(&hist[(int)(k >> shift) & 255], 1);
       });
       __syncthreads();
       int total;
-      const int cnt = hist[255 - tid], inc = block_scan(cnt, warp_sum, total);
+      const int cnt = tid < 256 ? hist[255 - tid] : 0, inc = block_scan(cnt, warp_sum, total);
       if (inc - cnt < need && need <= inc) {
         s_bin = 255 - tid;
         s_above = inc - cnt;
@@ -323,10 +344,10 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
     }
     // the page of the need-th of the keys equal to it
     int eq = 0, total;
-    each([&](int, unsigned long long k) { eq += k == thr; });
+    each([&](int, unsigned long long k, int) { eq += k == thr; });
     int before = block_scan(eq, warp_sum, total) - eq;
     if (before < need && need <= before + eq) {
-      each([&](int j, unsigned long long k) {
+      each([&](int j, unsigned long long k, int) {
         if (k == thr && ++before == need) s_page = j;
       });
       s_key = thr;
@@ -337,9 +358,9 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
   const unsigned long long key = s_key;
   const int last = s_page;
   int mine = 0, total;
-  each([&](int j, unsigned long long k) { mine += k > key || (k == key && j <= last); });
+  each([&](int j, unsigned long long k, int) { mine += k > key || (k == key && j <= last); });
   int at = block_scan(mine, warp_sum, total) - mine;
-  each([&](int j, unsigned long long k) {
+  each([&](int j, unsigned long long k, int) {
     if (k > key || (k == key && j <= last)) out[at++] = j;
   });
 }
@@ -416,6 +437,6 @@ extern "C" vkv_status vkv_page_select(const vkv_page_select_args* a, vkv_stream_
     }
     if (launch_ahead(score, grid, dim3((unsigned)warps * 32), smem, st, p) != cudaSuccess) return VKV_ERR_CUDA;
   }
-  return launch_ahead(page_pick_kernel, dim3((unsigned)seqs), dim3(kPickThreads), 0, st, p) == cudaSuccess ? VKV_OK
-                                                                                                       : VKV_ERR_CUDA;
+  auto pick = a->W <= 2 * kPickThreads ? page_pick_kernel<2> : a->W <= 8 * kPickThreads ? page_pick_kernel<8> : page_pick_kernel<0>;
+  return launch_ahead(pick, dim3((unsigned)seqs), dim3(kPickThreads), 0, st, p) == cudaSuccess ? VKV_OK : VKV_ERR_CUDA;
 }

@@ -255,6 +255,28 @@ def test_select(R, H, Hkv, d, P, W, topk, first, last, qt):
     assert np.array_equal(sel.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("W", [1500, 2048, 2049, 5000, 8193, 20000])
+@pytest.mark.parametrize("scores", ["spread", "few", "equal"])
+def test_select_wide_tables(W, scores):
+    """Tables of each width that the ranking treats differently, with rows that fill them and rows that
+    do not; scores of a handful of values (long runs of ties), or all equal."""
+    P, Hkv, d = 2, 2, 64
+    gen = torch.Generator(device=DEV).manual_seed(W)
+    lens = [W * P, 40 * P, W * P // 3, 0]
+    kbar = torch.zeros((300, Hkv, d), device=DEV)
+    if scores == "spread":
+        kbar.normal_(generator=gen)
+    elif scores == "few":
+        kbar[:, :, 0] = torch.randint(0, 4, (300, Hkv), device=DEV, generator=gen).float()
+    table = torch.randint(0, 300, (len(lens), W), dtype=torch.int32, device=DEV, generator=gen)
+    q = torch.rand((len(lens), 4, d), device=DEV, generator=gen).to(torch.bfloat16) + 0.5
+    for topk, first, last in ((1, 0, 0), (33, 2, 3), (700, 1, 0)):
+        err = new_err()
+        sel = vkv.page_select(q, kbar, table, i32(lens), P, topk, first, last, err=err)
+        want = oracle.page_select(f64(q), f64(kbar), table.cpu().numpy(), lens, P, topk, first, last)
+        assert int(err.item()) == 0 and np.array_equal(sel.cpu().numpy(), want), topk
+
+
 def test_select_infinities_nan_and_bad_pages():
     N, W, P = 40, 30, 8
     gen = torch.Generator(device=DEV).manual_seed(3)
