@@ -44,11 +44,10 @@ constexpr int kMaxBlocks = kMaxBlocksPerSm * kMaxCtas;
 constexpr float kSlack = 4.f;  // log2: how far a score may exceed the running maximum
 // The least share of a warp, tiles: a share of t tiles takes t times a tile's time and leaves
 // (tiles of the unit) / t parts to join, so the best t grows with the root of the unit's tiles
-// (one row of 131072 tokens, one head: 39 us with these factors, 54 with 4 tiles; 4 key heads of
-// 9097 tokens 23 and 27; one row of 1560 tokens 14 with 2 tiles, 16.5 with 4).  Chunks of 16 heads
-// have twice the joins per warp.
+// (one row of 131072 tokens: one head 36 us with this factor, 40 with its double, 54 with 4 tiles
+// throughout; 16 heads of one key head 49, 52 with the triple)
 constexpr int kMinTiles = 2;
-constexpr float kShareRoot[2] = {0.045f, 0.14f};  // for chunks of 8 and of 16 heads
+constexpr float kShareRoot = 0.045f;
 // Calls of at most this many tiles per warp give each unit whole blocks (two rows of 520 tokens,
 // 8 key heads of 64 channels: 9.8 us, on the line 16.3; one row of 1560 tokens 12.0 and 14.1; above
 // it equal shares count for more)
@@ -312,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
   if (all == 0) return;
   longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-  const int least = max(kMinTiles, (int)sqrtf(kShareRoot[NT - 1] * (float)longest));
+  const int least = max(kMinTiles, (int)sqrtf(kShareRoot * (float)longest));
   // Small calls: whole blocks per unit (of shares of `tb` / kWarps tiles at most), if the grid has
   // that many blocks
   int tb = 0, nb = 0;  // tiles of a block, or 0; blocks of the lane's rows, per unit

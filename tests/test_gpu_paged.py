@@ -445,6 +445,26 @@ def test_attn_long_rows(H, Hkv, n, kv):
     run_attn(R=2, H=H, Hkv=Hkv, d=128, P=64, lens=[n, 700], kv=kv)
 
 
+@pytest.mark.parametrize("q, kv", TYPE_PAIRS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("R, H, Hkv, hi", [(150, 20, 4, 500), (150, 48, 4, 300), (100, 8, 2, 500), (100, 24, 2, 900), (500, 4, 4, 90)])
+def test_attn_batches(q, kv, d, R, H, Hkv, hi):
+    """Rows times key heads above and below the number of blocks: equal shares that cut rows, and
+    whole blocks of more than 32 rows; pairs of key heads where rows are of 128 bytes."""
+    g = np.random.default_rng(R + H)
+    lens = [int(n) for n in g.integers(-1, hi + 1, R)]
+    lens[0], lens[7], lens[R - 1] = hi, 0, -1
+    run_attn(R=R, H=H, Hkv=Hkv, d=d, P=16, lens=lens, q=q, kv=kv, seed=R)
+
+
+@pytest.mark.parametrize("H, Hkv, d, kv, lens", [
+    (4, 4, 64, "bf16", [70000, 41, 60000]), (8, 2, 128, "e4m3", [130001, 7, 120000]), (36, 3, 64, "fp16", [64000, 50001]),
+    (4, 2, 128, "fp16", [60000, 33, 61111]), (10, 1, 128, "e4m3", [160000, 170001])])
+def test_attn_shares_of_long_rows(H, Hkv, d, kv, lens):
+    """More tiles per warp than calls of whole blocks have: few rows, cut many times."""
+    run_attn(R=len(lens), H=H, Hkv=Hkv, d=d, P=64, lens=lens, q="bf16" if kv != "fp16" else "fp16", kv=kv, poison=False)
+
+
 def test_attn_all_idle_and_all_empty():
     run_attn(R=3, H=4, Hkv=2, d=64, P=16, lens=[-1, -1, -1])
     run_attn(R=3, H=4, Hkv=2, d=64, P=16, lens=[0, 0, 0])
