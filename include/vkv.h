@@ -580,7 +580,7 @@ vkv_status vkv_page_map(const vkv_page_map_args* args, vkv_stream_t stream);
  * the mean of what it then holds up to there.
  */
 typedef struct {
-  int32_t T, Hkv, d;       /* tokens >= 0; key heads; d in {64, 128}                  */
+  int32_t T, Hkv, d;       /* tokens, 0..2^30; key heads, 1..4096; d in {64, 128}     */
   int32_t page, n_pages;   /* tokens per page; pages of the cache                     */
   int32_t x_dtype;         /* VKV_BF16 or VKV_FP16: k_new, v_new                      */
   int32_t kv_dtype;        /* x_dtype or VKV_E4M3: the cache                          */
@@ -652,9 +652,9 @@ vkv_status vkv_page_select(const vkv_page_select_args* args, vkv_stream_t stream
  * share one.
  */
 typedef struct {
-  int32_t R, H, Hkv, d;    /* rows; query heads (a multiple of Hkv); key heads; 64 or 128 */
+  int32_t R, H, Hkv, d;    /* rows; query heads (a multiple of Hkv, <= 4096); key heads; 64 or 128 */
   int32_t page, n_pages;
-  int32_t W;               /* table columns; R * W < 2^31, W * page < 2^31            */
+  int32_t W;               /* table columns; R * W < 2^31, W * page and topk * page < 2^31 - 64 */
   int32_t q_dtype;         /* VKV_BF16 or VKV_FP16: q and o                           */
   int32_t kv_dtype;        /* q_dtype or VKV_E4M3                                     */
   float scale;             /* > 0                                                     */

@@ -297,6 +297,40 @@ def test_select_infinities_nan_and_bad_pages():
     assert int(err.item()) == vkv.DEVERR_BAD_OFFSETS and (sel == -1).all()
 
 
+def test_select_streams_and_captured_graphs():
+    """Calls at the same time on two streams, and two graphs replayed at the same time, do not share scores."""
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    P, W, topk = 4, 3000, 50
+    cases = []
+    for i in range(2):
+        kbar = torch.randn((500, 4, 64), device=DEV, generator=gen)
+        table = torch.randint(0, 500, (6, W), dtype=torch.int32, device=DEV, generator=gen)
+        q = torch.randn((6, 8, 64), device=DEV, generator=gen).to(torch.bfloat16)
+        cases.append((q, kbar, table, i32([W * P, 900, 0, -1, 5000 + i, 7777]), P, topk, 1, 2))
+    want = [vkv.page_select(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(vkv.page_select(*cases[i]))
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(vkv.page_select(*c))
+        graphs.append(g)
+    for _ in range(10):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i] + [outs[i]])
+
+
 # ---------------------------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------------------------
