@@ -59,7 +59,6 @@ __device__ __forceinline__ int ring_start(long long t, int n) {
 
 template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p) {
-  griddep_launch_dependents();
   griddep_wait();
   extern __shared__ int sm[];
   int* tok = sm;               // [R + 1] new tokens before row r
@@ -224,6 +223,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
       if (p.pos) p.pos[i] = in ? t[e] : -1;
     }
   }
+  griddep_launch_dependents();
 }
 
 }  // namespace
