@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
   if (all == 0) return;
   longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-  const int least = max(kMinTiles, (int)sqrtf(kShareRoot * (float)longest));
+  const int root = max(1, (int)sqrtf(kShareRoot * (float)longest)), least = max(kMinTiles, root);
   // Small calls: whole blocks per unit (of shares of `tb` / kWarps tiles at most), if the grid has
   // that many blocks
   int tb = 0, nb = 0;  // tiles of a block, or 0; blocks of the lane's rows, per unit
@@ -319,7 +319,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     const int units = p.Hkv * p.n_chunks;
     const long long even = quotient(all * units + gridDim.x * kWarps - 1, (long long)gridDim.x * kWarps);
     if (even <= kWholeMost && (long long)p.R * units <= 4 * kMaxBlocks) {
-      const int s0 = max(least, (int)even);
+      // (single tiles where a unit needs several blocks anyway: two rows of 520 tokens 9.2 and 8.8 us,
+      // 42 rows of up to 456 tokens 12.6 and 11.6)
+      const int s0 = max(longest > kMinTiles * kWarps ? root : least, (int)even);
 #pragma unroll 1
       for (int s = s0; s <= s0 + 1 + s0 / 4; ++s) {
         nb = 0;
@@ -1083,7 +1085,7 @@ extern "C" vkv_status vkv_page_attn(const vkv_page_attn_args* a, vkv_stream_t st
   const long long most = a->sel ? std::min<long long>((long long)a->topk * a->page, (long long)a->W * a->page)
                          : a->window > 0 ? std::min<long long>((long long)a->sink + a->window, (long long)a->W * a->page)
                                          : (long long)a->W * a->page;
-  const long long row_blocks = (std::max<long long>(1, (most + tt - 1) / tt) + kMinTiles * kWarps - 1) / (kMinTiles * kWarps);
+  const long long row_blocks = (std::max<long long>(1, (most + tt - 1) / tt) + kWarps - 1) / kWarps;
   const int blocks = (int)std::min<long long>(all, row_blocks * a->R * a->Hkv * p.n_chunks);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t rc = a->d == 128 ? launch_d<128>(p, a->q_dtype, a->kv_dtype, blocks, n_sm, dev, st)
