@@ -44,8 +44,8 @@ constexpr int kMaxBlocks = kMaxBlocksPerSm * kMaxCtas;
 constexpr float kSlack = 4.f;  // log2: how far a score may exceed the running maximum
 // The least share of a warp, tiles: a share of t tiles takes t times a tile's time and leaves
 // (tiles of the unit) / t parts to join, so the best t grows with the root of the unit's tiles
-// (one row of 131072 tokens: one head 36 us with this factor, 40 with its double, 54 with 4 tiles
-// throughout; 16 heads of one key head 49, 52 with the triple)
+// (one row of 131072 tokens, one head: 36 us with this factor, 40 with its double, 54 with 4 tiles
+// throughout)
 constexpr int kMinTiles = 2;
 constexpr float kShareRoot = 0.045f;
 // Calls of at most this many tiles per warp give each unit whole blocks (two rows of 520 tokens,
