@@ -667,7 +667,8 @@ typedef struct {
   int64_t table_stride;
   const int32_t* kv_len;   /* DEVICE [R]                                              */
   const int32_t* sel;      /* optional DEVICE [R][Hkv][topk]: distinct logical pages, of which the
-                              first min(topk, ceil(kv_len / page)) are read; -1 = none; needs window = 0 */
+                              first min(topk, ceil(kv_len / page)) are read; -1 = none; needs window = 0.
+                              NULL means no selection: rows that select nothing pass entries of -1 */
   const float* k_scale;    /* DEVICE [Hkv], VKV_E4M3 only (NULL = 1)                  */
   const float* v_scale;
   float* lse;              /* DEVICE [R][H]                                           */

@@ -299,6 +299,8 @@ PyObject* page_attn(PyObject*, PyObject* const* x, Py_ssize_t n) {
     if (x[10] != Py_None) {
       const at::Tensor& sel = tensor(x[10], "sel");
       a.topk = size_of(sel.dim() == 3 ? sel.size(2) : -1, "sel");
+      // an empty tensor has no address, which the entry point would take for no selection
+      if (a.topk == 0) throw Refusal{"sel must have at least one entry per row and key head"};
       a.sel = vec<int32_t>(x[10], "sel", at::kInt, {R, c.Hkv, a.topk}, dev);
     }
     scales_of(x[11], x[12], c, dev, &a.k_scale, &a.v_scale);
