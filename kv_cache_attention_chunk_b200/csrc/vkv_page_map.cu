@@ -11,6 +11,7 @@
 // dependent reads (lengths, then ring or table) and the stores.  A thread takes kTok tokens
 // at a time, so that their bisections and look-ups overlap.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstring>
 
@@ -240,7 +241,8 @@ extern "C" vkv_status vkv_page_map(const vkv_page_map_args* a, vkv_stream_t stre
   if (!a->kv_len || !a->new_len || !a->table || !a->ring || !a->ring_pos || !a->kv_len_out || !a->ring_pos_out ||
       !a->slot)
     return VKV_ERR_NULL;
-  const int n_sm = device_sm_count(nullptr);
+  int dev = 0;
+  const int n_sm = device_sm_count(&dev);
   if (n_sm <= 0) return VKV_ERR_CUDA;
   MapParams p;
   std::memset(&p, 0, sizeof(p));
@@ -273,10 +275,17 @@ extern "C" vkv_status vkv_page_map(const vkv_page_map_args* a, vkv_stream_t stre
   const int ctas = (int)std::min<long long>(most, (items + kMapThreads - 1) / kMapThreads);
   const size_t smem = (size_t)(4 * a->R + 3) * sizeof(int);
   auto fn = in_place ? page_map_kernel<true> : page_map_kernel<false>;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return VKV_ERR_CUDA;
+  // the limit is the kernel's, whoever calls it: raised once per device, to the most any call takes (set to
+  // each call's own need, it could fall below a larger call's on another thread, before that one's launch)
+  static std::atomic<uint64_t> ready[2];  // by kernel: devices (by bit) on which it is raised
+  std::atomic<uint64_t>& rd = ready[in_place ? 1 : 0];
+  if (smem > 48 * 1024 && !(rd.load(std::memory_order_acquire) >> dev & 1u)) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (4 * VKV_PAGE_MAX_ROWS + 3) * (int)sizeof(int)) != cudaSuccess) {
+      cudaGetLastError();
+      return VKV_ERR_CUDA;
+    }
+    rd.fetch_or(1ull << dev, std::memory_order_release);
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (!in_place || ctas == 1)  // one block needs no cluster (a cluster launch takes a microsecond more)

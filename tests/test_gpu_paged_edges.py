@@ -25,3 +25,32 @@ def test_attn_refuses_an_empty_selection():
         for window in (0, 7):
             with pytest.raises(ValueError, match="sel"):
                 attn_call({**c, "sel": sel, "window": window})
+
+
+def test_map_from_several_threads_with_different_row_counts():
+    """Calls with more rows than 48 KB of shared memory hold, from several threads at once."""
+    failed = []
+
+    def loop(R):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            kv, new = torch.zeros(R, dtype=torch.int32, device=DEV), torch.ones(R, dtype=torch.int32, device=DEV)
+            table, ring = torch.full((R, 1), -1, dtype=torch.int32, device=DEV), torch.arange(R, dtype=torch.int32, device=DEV)
+            pos, slot = torch.tensor([0, R], device=DEV), torch.zeros(R, dtype=torch.int64, device=DEV)
+            kv_out, pos_out = torch.empty_like(kv), torch.empty_like(pos)
+            a = vkv.vkv_page_map_args(R, 1, 16, R, R, 0)
+            a.kv_len, a.new_len, a.table, a.table_stride = kv.data_ptr(), new.data_ptr(), table.data_ptr(), 1
+            a.ring, a.ring_pos, a.kv_len_out, a.ring_pos_out = (x.data_ptr() for x in (ring, pos, kv_out, pos_out))
+            a.slot = slot.data_ptr()
+            stream.synchronize()
+            got = [vkv.vkv_page_map(a, stream.cuda_stream) for _ in range(3000)]
+            stream.synchronize()
+            if any(got) or not torch.equal(slot, 16 * torch.arange(R, device=DEV)):
+                failed.append((R, sum(map(bool, got))))
+
+    threads = [threading.Thread(target=loop, args=(R,)) for R in (4096, 3200, 3900, 3300, 4000, 3100)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
