@@ -71,7 +71,10 @@ inline FastDiv fast_div(int d) {
 }
 
 // Launches a kernel that calls griddep_wait() before it touches memory: its blocks may take
-// their places while the stream's last kernel ends (programmatic dependent launch).  The
+// their places while the stream's last kernel ends (programmatic dependent launch).
+// All its loads are ordinary ones, never the read-only path's: that is for memory which nobody
+// writes while the kernel is there, and here the last kernel may still be writing lengths, table,
+// selection or queries; the compiler may also move such a load ahead of the wait.  The
 // kernels let the next one in with griddep_launch_dependents() once their loads are done, not
 // when they begin: waiting blocks hold shared memory, several launches pile up, and what comes
 // next is crowded onto few SMs (one row of 1560 tokens 12 us if let in at the start, 10.7 at the

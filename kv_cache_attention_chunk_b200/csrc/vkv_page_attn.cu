@@ -269,13 +269,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   __shared__ int4 pending[4];
   __shared__ int s_last[4];
 
-  griddep_wait();  // launched ahead of the end of the stream's last kernel
+  griddep_wait();  // launched ahead of the end of the stream's last kernel: see launch_ahead on its loads
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
   // a row's visible tokens: x in [0, n) is token x (x < lo) or x + gap, or token x % page of
   // selected page x / page
   auto row_len = [&](int r) {
-    const int len = __ldg(p.kv_len + r);
+    const int len = p.kv_len[r];
     return len >= -1 && (long long)len <= (long long)p.W * p.page ? len : -2;
   };
   auto visible = [&](int len, int& lo, int& gap) {
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
         int j, tok;
         if (p.sel) {
           const int e = p.by_page(x);
-          j = __ldg(p.sel + ((long long)cr * p.Hkv + head) * p.topk + e);
+          j = p.sel[((long long)cr * p.Hkv + head) * p.topk + e];
           nx_off = x - e * p.page;
           if (j < 0 || j >= p.W) {
             if (j != -1 && p.err) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
           j = p.by_page(tok);
           nx_off = tok - j * p.page;
         }
-        if (nx_want) nx_page = __ldg(p.table + cr * p.table_stride + j);
+        if (nx_want) nx_page = p.table[cr * p.table_stride + j];
       }
       --todo;
       if (++ct == tiles) {
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     float m[NT][2], l[NT][2], acc[NT][D / 16][4];
     auto load_q = [&](int r, int h, int hc0, int n_heads) {
       const T* q = reinterpret_cast<const T*>(p.q) + r * p.q_sb + (long long)(h * p.G + hc0) * p.q_sh;
-      const float c0 = p.scale_log2 * (F8 && p.ks ? __ldg(p.ks + h) : 1.f);
+      const float c0 = p.scale_log2 * (F8 && p.ks ? p.ks[h] : 1.f);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int hd = nt * 8 + g8;
@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
         for (int c = 0; c < D / 16; ++c) {
           // an 8-bit row's fragment has channels 16 c + 4 t4 ..+3, a 16-bit row's 16 c + 2 t4, +1, +8, +9
           const int d0 = 16 * c + (F8 ? 4 * t4 : 2 * t4), d1 = d0 + (F8 ? 2 : 8);
-          qf[nt][c][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d0)) : 0u;
-          qf[nt][c][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d1)) : 0u;
+          qf[nt][c][0] = in ? *reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d0) : 0u;
+          qf[nt][c][1] = in ? *reinterpret_cast<const uint32_t*>(q + hd * p.q_sh + d1) : 0u;
         }
         float inv = 1.f;
         if constexpr (F8 && std::is_same<T, __nv_bfloat16>::value) {
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], o);
         if (unit_begin && (flags & 8)) {  // the whole unit
-          const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
+          const float vs = F8 && p.vs ? p.vs[h] : 1.f;
           T* o = reinterpret_cast<T*>(p.o) + r * p.o_sb + (long long)(h * p.G + hc0) * p.o_sh;
           float* lse = p.lse + (size_t)r * p.H + h * p.G + hc0;
 #pragma unroll
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     const int te = __shfl_sync(0xFFFFFFFFu, mp.te, 31 - __clz(grp));
     const int h = u / p.n_chunks, hc0 = (u - h * p.n_chunks) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
     const bool whole = t0 == 0 && te == tiles;
-    const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
+    const float vs = F8 && p.vs ? p.vs[h] : 1.f;
     const size_t ws = (((size_t)(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) << jp) + (h & jp)) * hcw;
     // the warps' parts of this unit (at most one each)
     const float* src[kWarps];
@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
     if (s_last[f]) {
       const int r = pending[f].x, h = pending[f].y >> 16, hc0 = (pending[f].y & 0xFFFF) * Z::HC, n_heads = min(Z::HC, p.G - hc0);
       const int n = pending[f].w, first = pending[f].z;
-      const float vs = F8 && p.vs ? __ldg(p.vs + h) : 1.f;
+      const float vs = F8 && p.vs ? p.vs[h] : 1.f;
       float top[HW], sum[HW];
       V4 x[HW];
       // part 0 lies among its block's lasts, the others among their blocks' firsts

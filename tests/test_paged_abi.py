@@ -4,6 +4,7 @@ Every request here is invalid on purpose, or valid on a machine without a GPU (V
 none reaches a kernel.
 """
 import ctypes
+import os
 
 import pytest
 import torch
@@ -157,3 +158,13 @@ def test_workspace_sizes():
     assert vkv.vkv_page_select_workspace_size(3, 8, 100) >= 3 * 8 * 100 * 8
     assert vkv.vkv_page_attn_workspace_size(7, 2, 128) == 0
     assert vkv.vkv_page_attn_workspace_size(8, 2, 96) == 0
+
+
+def test_kernels_launched_ahead_load_coherently():
+    """Read-only-path loads are for memory that nobody writes while the kernel is resident: a kernel that
+    takes its place while the stream's last one still runs has none."""
+    for name in ("vkv_page.cuh", "vkv_page_map.cu", "vkv_page_append.cu", "vkv_page_select.cu", "vkv_page_attn.cu"):
+        with open(os.path.join(build.CSRC, name)) as f:
+            text = f.read()
+        for word in ("__ldg", "global.nc", "__restrict__"):
+            assert word not in text, (name, word)
