@@ -33,21 +33,24 @@ struct AppendParams {
 // processor, 1990), two values an instruction, where a division takes about ten.  Chunks with
 // infinities or quotients that could pass 1e30, and s outside [2^-60, 2^60], where remainders
 // could underflow, are divided.
+// Both work on -x and give (-x) (-r) corrected by (q s - x) (-r): an exact remainder is +0
+// whatever the signs of its terms, and with these the quotient -0 of x = -0 stays -0 where x r
+// corrected by (x - q s) r would become +0 (s > 0; a scale below zero is divided by as well).
 struct Divisor {
-  float s, r;
-  uint64_t s2, r2;  // -s and r, twice each
+  float s, r;       // the scale, -1 / scale
+  uint64_t s2, r2;  // the same, twice each
   bool plain;
   __device__ __forceinline__ explicit Divisor(float scale) {
     s = scale;
-    r = __fdiv_rn(1.f, scale);
-    s2 = pack2f(-s, -s);
+    r = __fdiv_rn(-1.f, scale);
+    s2 = pack2f(s, s);
     r2 = pack2f(r, r);
-    const float a = fabsf(scale);
-    plain = !(a >= 0x1p-60f && a <= 0x1p60f);
+    plain = !(scale >= 0x1p-60f && scale <= 0x1p60f);
   }
   template <typename IN>
   __device__ __forceinline__ void operator()(const uint4 x, float* f) const {
-    unpack8<IN>(x, f);
+    constexpr uint32_t kSigns = 0x80008000u;
+    unpack8<IN>(make_uint4(x.x ^ kSigns, x.y ^ kSigns, x.z ^ kSigns, x.w ^ kSigns), f);
     // the largest magnitude (NaN aside): the sign-free patterns are ordered like the values
     const uint32_t m01 = __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), m23 = __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu);
     const uint32_t m = __vmaxu2(m01, m23);
@@ -61,7 +64,7 @@ struct Divisor {
     if (plain || !(top * fabsf(r) < 1e30f)) {
 #pragma unroll 1
       for (int e = 0; e < 8; ++e) {  // rotates, so that no register is indexed
-        const float t = __fdiv_rn(f[0], s);
+        const float t = __fdiv_rn(f[0], -s);
 #pragma unroll
         for (int k = 0; k < 7; ++k) f[k] = f[k + 1];
         f[7] = t;

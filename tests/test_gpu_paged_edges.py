@@ -27,6 +27,23 @@ def test_attn_refuses_an_empty_selection():
                 attn_call({**c, "sel": sel, "window": window})
 
 
+@pytest.mark.parametrize("x", ["bf16", "fp16"])
+@pytest.mark.parametrize("means", [False, True])
+def test_append_e4m3_keeps_the_sign_of_zero(x, means):
+    """x / scale is -0 for x = -0 (and for +0 over a negative scale), and e4m3 has both zeros."""
+    scale = torch.tensor([0.5, 0.3, 3.0, 2.0**-70, -0.7, 1.0], device=DEV)
+    new = torch.zeros((3, 6, 64), dtype=TYPES[x], device=DEV)
+    new[:, :, ::3] = -0.0
+    new[1, :, 5] = -6.0e-8  # a quotient that rounds to -0 (or not, over a small scale)
+    k, v = (torch.ones((2, 4, 6, 64), device=DEV).to(torch.float8_e4m3fn) for _ in range(2))
+    kbar = torch.zeros((2, 6, 64), device=DEV) if means else None
+    vkv.page_append(new, new, torch.tensor([4, 5, 6], device=DEV), k, v, k_scale=scale, v_scale=scale, kbar=kbar)
+    want = (new.float() / scale[None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    assert int((bits(want) == 0x80).sum()) > 100
+    for got in (k, v):
+        assert torch.equal(bits(got[1, :3]), bits(want))
+
+
 def test_map_from_several_threads_with_different_row_counts():
     """Calls with more rows than 48 KB of shared memory hold, from several threads at once."""
     failed = []
