@@ -258,8 +258,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
   using Z = Shape<D, F8, NT>;
   using M = typename std::conditional<F8, __half, T>::type;  // operand type of the products
   // f16 weights use the exponents above 1: with 2^11 for the running maximum, what is below
-  // f16's smallest step is below 2^-36 of it
-  constexpr float kShift = std::is_same<M, __half>::value ? 11.f : 0.f;
+  // f16's smallest step is below 2^-36 of it.  bf16 has the exponents below 1: with 2^-kSlack no weight
+  // exceeds 1, so that values near the type's largest are not multiplied past fp32's
+  constexpr float kShift = std::is_same<M, __half>::value ? 11.f : -kSlack;
   using V4 = typename Vec<D>::type;
   constexpr int VL = D / 32;  // floats of V4
   extern __shared__ __align__(256) char smem[];

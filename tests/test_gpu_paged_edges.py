@@ -44,6 +44,27 @@ def test_append_e4m3_keeps_the_sign_of_zero(x, means):
         assert torch.equal(bits(got[1, :3]), bits(want))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_bf16_values_near_the_largest(d):
+    """A finite output of bf16 values near the type's largest: weights stay at 1 or below, also
+    where a score exceeds the running maximum by less than what moves it."""
+    R, Hkv, P, n = 8, 8, 16, 2048
+    N = R * n // P
+    k, v = (torch.zeros((N, P, Hkv, d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    table = torch.arange(N, dtype=torch.int32, device=DEV).view(R, n // P)
+    for r in range(R):
+        for h in range(Hkv):  # one token with a score of 2.08 among zeros, at another place in each row and head
+            t = 40 + 16 * (r * Hkv + h)
+            k[table[r, t // P], t % P, h, 0] = 2.078125
+            v[table[r, t // P], t % P, h] = 3.0e38 * (-1) ** h
+    q = torch.zeros((R, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = 1.0
+    o, lse = vkv.page_attn(q, k, v, table, i32([n] * R), scale=1.0)
+    assert o.isfinite().all()
+    ref = oracle.page_attn(f64(q), f64(k), f64(v), table.cpu().numpy(), [n] * R, 1.0)
+    check_attn(o, lse, ref, "bf16", d)
+
+
 def test_map_from_several_threads_with_different_row_counts():
     """Calls with more rows than 48 KB of shared memory hold, from several threads at once."""
     failed = []
