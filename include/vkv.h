@@ -603,8 +603,8 @@ vkv_status vkv_page_append(const vkv_page_append_args* args, vkv_stream_t stream
  *   score(g, j) = < sum of the queries of the heads that share key head g, kbar[table[r][j]][g] >
  * (fp64; a positive factor does not change the ranking; equal scores keep the lower j
  * first; NaN ranks last), min(topk, n) pages in all.  sel receives their logical numbers
- * j in ascending order, then -1.  A table entry outside [0, n_pages) raises
- * VKV_DEVERR_BAD_INDEX and ranks last; a length below -1 or above W * page raises
+ * j in ascending order, then -1.  A table entry of the row's n that lies outside [0, n_pages)
+ * raises VKV_DEVERR_BAD_INDEX and ranks last; a length below -1 or above W * page raises
  * VKV_DEVERR_BAD_OFFSETS and counts as 0.  Rows of length 0 or -1 get -1 throughout.
  */
 typedef struct {

@@ -221,7 +221,13 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelParams
   for (int i = kept + tid; i < p.topk; i += kPickThreads) out[i] = -1;
   if (n <= p.topk) {
     if (p.W <= p.topk && tid == 0) page_row_len(raw, p.W, p.page, p.err);  // no score kernel has run
-    for (int i = tid; i < n; i += kPickThreads) out[i] = i;
+    // the row's pages are all kept and no score was taken: its first key head looks at their numbers
+    const int* tab = p.table + r * p.table_stride;
+    const bool look = p.err && blockIdx.x == r * p.Hkv;
+    for (int i = tid; i < n; i += kPickThreads) {
+      out[i] = i;
+      if (look && (tab[i] < 0 || tab[i] >= p.n_pages)) atomicCAS(p.err, 0, VKV_DEVERR_BAD_INDEX);
+    }
     return;
   }
   const unsigned long long* keys = p.keys + (size_t)blockIdx.x * p.W;

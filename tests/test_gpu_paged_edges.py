@@ -92,3 +92,25 @@ def test_map_from_several_threads_with_different_row_counts():
     for t in threads:
         t.join()
     assert not failed
+
+
+def test_select_checks_the_pages_of_short_rows():
+    """A row whose pages are all kept is not ranked, but a page number outside the cache is still reported."""
+    N, P, W = 9, 4, 6
+    kbar, q = torch.ones((N, 3, 64), device=DEV), torch.ones((3, 3, 64), dtype=torch.bfloat16, device=DEV)
+    for bad in (-1, N, -(2**31)):
+        for row, col in ((0, 0), (0, 2), (2, 3)):
+            table = torch.zeros((3, W), dtype=torch.int32, device=DEV)
+            table[row, col] = bad
+            for topk in (4, 6, 9):  # fewer than the table's columns: some other row could be ranked
+                err = new_err()
+                sel = vkv.page_select(q, kbar, table, i32([9, 0, 13]), P, topk, err=err)
+                assert int(err.item()) == vkv.DEVERR_BAD_INDEX
+                assert sel[0, 1].tolist() == [0, 1, 2] + [-1] * (topk - 3)
+                assert sel[2, 2].tolist() == [0, 1, 2, 3] + [-1] * (topk - 4)
+    table = torch.zeros((3, W), dtype=torch.int32, device=DEV)
+    table[0, 3:], table[1], table[2, 4:] = -1, -1, N  # columns behind the rows' pages are not looked at
+    for topk in (4, 6, 9):
+        err = new_err()
+        vkv.page_select(q, kbar, table, i32([9, 0, 13]), P, topk, err=err)
+        assert int(err.item()) == 0
