@@ -755,6 +755,7 @@ def latent_attn(q, kv, d_c, scale=None, kr=None, err=None, stream=None, out=None
 # ---------------------------------------------------------------------------
 # These calls run once per layer and token; their arguments are checked and marshalled by
 # csrc/vkv_binding.cpp (a refused one is a ValueError), which calls the same entry points.
+# With `stream`, the caller orders the inputs before that stream and that stream before what uses the results.
 _page_attn_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, cleared once (the call leaves it clear)
 _NO_WORKSPACE = torch.empty(0, dtype=torch.uint8)
 _page_select_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, grown on demand
@@ -797,6 +798,25 @@ def _handle(di, stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _stream_of(di, sh):
+    """The torch stream of a handle on device `di`."""
+    return torch.cuda.ExternalStream(sh, device=di) if sh else torch.cuda.default_stream(di)
+
+
+def _new_outputs(x, stream, *specs):
+    """Tensors (shape, type) on the device of `x` for a call on `stream` to write: memory of that stream
+    (what the current stream last used could still be written there), and not handed out again, once they
+    are freed, before the current stream is done with what it has of them by then."""
+    di = x.get_device()
+    if stream is None or di < 0 or _handle(di, stream) == torch._C._cuda_getCurrentRawStream(di):
+        return [torch.empty(shape, dtype=t, device=x.device) for shape, t in specs]
+    with torch.cuda.stream(_stream_of(di, _handle(di, stream))):
+        out = [torch.empty(shape, dtype=t, device=x.device) for shape, t in specs]
+    for y in out:
+        y.record_stream(torch.cuda.current_stream(di))
+    return out
+
+
 def page_map(kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens, out=None, err=None, stream=None):
     """Pages and slots of one step's new tokens (vkv_page_map).
 
@@ -809,10 +829,9 @@ def page_map(kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens
     not fit changes nothing and sets err.
     """
     if out is None:
-        R, i32, i64 = kv_len.shape[0], dict(dtype=torch.int32, device=kv_len.device), dict(dtype=torch.int64, device=kv_len.device)
-        out = {"kv_len": torch.empty(R, **i32), "ring": torch.empty(2, **i64), "slot": torch.empty(max_tokens, **i64),
-               "row": torch.empty(max_tokens, **i32), "pos": torch.empty(max_tokens, **i32),
-               "cu": torch.empty(R + 1, **i32)}
+        R, i32, i64 = kv_len.shape[0], torch.int32, torch.int64
+        out = dict(zip(("kv_len", "ring", "slot", "row", "pos", "cu"), _new_outputs(
+            kv_len, stream, (R, i32), (2, i64), (max_tokens, i64), (max_tokens, i32), (max_tokens, i32), (R + 1, i32))))
     get = out.get
     _page_call("page_map", kv_len, stream, kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens,
                out["kv_len"], out["ring"], out["slot"], get("row"), get("pos"), get("cu"), err)
@@ -843,8 +862,7 @@ def _page_workspace(kept, di, sh, need, clear):
         return _NO_WORKSPACE  # what makes the call refuse its arguments comes first
     if sh != torch._C._cuda_getCurrentRawStream(di) or di != torch._C._cuda_getDevice():
         # allocate, clear and ask about a capture on the stream that will use it
-        on = torch.cuda.ExternalStream(sh, device=di) if sh else torch.cuda.default_stream(di)
-        with torch.cuda.stream(on):
+        with torch.cuda.stream(_stream_of(di, sh)):
             return _page_workspace(kept, di, sh, need, clear)
     if torch._C._cuda_isCurrentStreamCapturing():
         return _new_workspace(di, need, clear)
@@ -862,7 +880,7 @@ def page_select(q, kbar, block_table, kv_len, page_size, topk, sink_pages=0, loc
     Returns int32 [R, Hkv, topk]: logical page numbers ascending, then -1.
     """
     R, Hkv = q.shape[0], kbar.shape[1]
-    sel = out if out is not None else torch.empty((R, Hkv, topk), dtype=torch.int32, device=q.device)
+    sel = out if out is not None else _new_outputs(q, stream, ((R, Hkv, topk), torch.int32))[0]
     if workspace is None:
         di = q.get_device()
         workspace = _page_workspace(_page_select_ws, di, _handle(di, stream),
@@ -885,7 +903,7 @@ def page_attn(q, k_pages, v_pages, block_table, kv_len, scale=None, sink=0, wind
     """
     R, H, d = q.shape
     if out is None:
-        out = torch.empty((R, H, d), dtype=q.dtype, device=q.device), torch.empty((R, H), dtype=torch.float32, device=q.device)
+        out = _new_outputs(q, stream, ((R, H, d), q.dtype), ((R, H), torch.float32))
     o, lse = out
     if workspace is None:
         di = q.get_device()

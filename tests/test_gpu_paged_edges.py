@@ -114,3 +114,48 @@ def test_select_checks_the_pages_of_short_rows():
         err = new_err()
         vkv.page_select(q, kbar, table, i32([9, 0, 13]), P, topk, err=err)
         assert int(err.item()) == 0
+
+
+def _calls(stream):
+    """Each call that makes its outputs itself, with its inputs ready: name -> (call, its outputs' expected values)."""
+    c = attn_case(R=2, H=8, Hkv=2, d=128, P=16, lens=[900, 33], poison=False)
+    kbar = torch.randn((c["k"].shape[0], 2, 128), device=DEV)
+    lens, one = i32(c["lens"]), i32([1, 1])
+    n = c["k"].shape[0]
+    table, ring, pos = torch.full((2, 4), 7, dtype=torch.int32, device=DEV), torch.arange(n, dtype=torch.int32, device=DEV), \
+        torch.tensor([0, n], device=DEV)
+    kv = i32([3, 5])
+    return {"attn": lambda **k: list(vkv.page_attn(c["q"], c["k"], c["v"], c["table"], lens, **k)),
+            "select": lambda **k: [vkv.page_select(c["q"], kbar, c["table"], lens, 16, 5, 1, 1, **k)],
+            "map": lambda **k: list(vkv.page_map(kv, one, table, ring, pos, 16, 2000, **k).values())}
+
+
+@pytest.mark.parametrize("name", ["attn", "select", "map"])
+def test_outputs_made_for_another_stream(name):
+    """Outputs that a call makes for `stream` are memory that no pending work of the current stream still
+    writes, and freeing them does not hand them out while the current stream still reads them."""
+    s = torch.cuda.Stream()
+    call = _calls(s)[name]
+    want = [x.clone() for x in call()]
+    torch.cuda.synchronize()
+    got = call(stream=s)  # workspaces and the like exist from here on
+    torch.cuda.synchronize()
+    del got
+    for _ in range(2):
+        torch.cuda._sleep(20_000_000)
+        junk = [torch.full_like(x, 99) for x in want]  # pending on the current stream, then free for its next allocations
+        del junk
+        got = call(stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del got
+    got = call(stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(20_000_000)
+    copies = [x.clone() for x in got]
+    del got
+    with torch.cuda.stream(s):
+        junk = [torch.full_like(x, 99) for x in want]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copies, want))
+    del junk
