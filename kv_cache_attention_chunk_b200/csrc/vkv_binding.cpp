@@ -86,6 +86,56 @@ void no_overlap(const at::Tensor& x, const char* what) {
   if (at::has_internal_overlap(x) == at::MemOverlap::Yes) throw Refusal{std::string(what) + " overlaps itself"};
 }
 
+// A tensor and the bytes between its first and behind its last element.
+struct Span {
+  const at::Tensor& x;
+  const char *begin, *end;
+  explicit Span(const at::Tensor& t) : x(t) {
+    const at::IntArrayRef size = x.sizes(), stride = x.strides();
+    int64_t last = 0;
+    for (size_t i = 0; i < size.size(); ++i) last += (size[i] - 1) * stride[i];
+    begin = static_cast<const char*>(x.const_data_ptr());
+    end = begin + (x.numel() ? (last + 1) * (int64_t)x.element_size() : 0);
+  }
+};
+
+// Whether sum_i x_i stride_i = off has a solution with |x_i| < size_i over the axes from `i` on (largest
+// stride first, `reach` the most that the axes behind an axis add up to): two equally strided views meet
+// there.  Strides of views into one dense buffer leave two candidates per axis at most; `budget` bounds others.
+bool meets(const int64_t* size, const int64_t* stride, const int64_t* reach, int n, int i, int64_t off, int& budget) {
+  if (i == n) return off == 0;
+  const int64_t s = stride[i], r = reach[i];
+  const auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+  const int64_t lo = std::max(-(size[i] - 1), floor_div(off - r + s - 1, s)), hi = std::min(size[i] - 1, floor_div(off + r, s));
+  for (int64_t x = lo; x <= hi && budget > 0; ++x)
+    if (--budget, meets(size, stride, reach, n, i + 1, off - x * s, budget)) return true;
+  return false;
+}
+
+// Whether an element of `a` certainly lies on one of `b`: exact for tensors without gaps and for two of equal
+// sizes and strides (two parts of one buffer, side by side or not); others count as apart.
+bool share_within(const Span& p, const Span& q) {
+  const at::Tensor &a = p.x, &b = q.x;
+  if (a.is_non_overlapping_and_dense() && b.is_non_overlapping_and_dense()) return true;
+  constexpr int kMost = 4;
+  if (a.sizes() != b.sizes() || a.dim() > kMost || a.element_size() != b.element_size()) return false;
+  int64_t size[kMost], stride[kMost], reach[kMost], n = 0;
+  for (int64_t i = 0; i < a.dim(); ++i) {
+    if (a.size(i) == 1) continue;
+    if (a.stride(i) != b.stride(i)) return false;
+    if (a.stride(i) == 0) continue;
+    int64_t at = n++;
+    for (; at > 0 && stride[at - 1] < a.stride(i); --at) size[at] = size[at - 1], stride[at] = stride[at - 1];
+    size[at] = a.size(i), stride[at] = a.stride(i);
+  }
+  int64_t sum = 0;
+  for (int64_t i = n; i-- > 0; sum += (size[i] - 1) * stride[i]) reach[i] = sum;
+  const int64_t e = (int64_t)a.element_size(), bytes = q.begin - p.begin;
+  int budget = 64;
+  return bytes % e == 0 && meets(size, stride, reach, (int)n, 0, bytes / e, budget);
+}
+inline bool share(const Span& p, const Span& q) { return p.begin < q.end && q.begin < p.end && share_within(p, q); }
+
 // [.., .., d] with contiguous d: outer and inner stride of a 3-d tensor
 vkv_tensor rows3(const at::Tensor& x, const char* what, int dev, bool outer_is_row) {
   if (x.dim() != 3 || !x.is_cuda() || x.get_device() != dev || x.stride(2) != 1)
@@ -225,8 +275,18 @@ PyObject* page_append(PyObject*, PyObject* const* x, Py_ssize_t n) {
     vkv_page_append_args a{};
     a.T = size_of(kn.size(0), "k_new");
     a.Hkv = c.Hkv, a.d = c.d, a.page = c.page, a.n_pages = c.n_pages;
-    no_overlap(tensor(x[5], "k_pages"), "k_pages");
-    no_overlap(tensor(x[6], "v_pages"), "v_pages");
+    const at::Tensor &k = tensor(x[5], "k_pages"), &v = tensor(x[6], "v_pages");
+    no_overlap(k, "k_pages");
+    no_overlap(v, "v_pages");
+    // one tensor may be both where it gets the same rows as both
+    const bool one = c.k.ptr == c.v.ptr && k.strides() == v.strides() && kn.const_data_ptr() == vn.const_data_ptr() &&
+                     kn.strides() == vn.strides() && x[7] == x[8];
+    const Span ks(k), vs(v);
+    if (!one && share(ks, vs)) throw Refusal{"k_pages and v_pages overlap, with unlike rows to store"};
+    if (x[9] != Py_None) {
+      const Span means(tensor(x[9], "kbar"));
+      if (share(means, ks) || share(means, vs)) throw Refusal{"kbar overlaps the cache"};
+    }
     a.x_dtype = dtype_of(kn, "k_new");
     a.kv_dtype = c.dtype;
     a.k_new = rows3(kn, "k_new", dev, false);

@@ -843,7 +843,8 @@ def page_append(k_new, v_new, slot, k_pages, v_pages, k_scale=None, v_scale=None
 
     k_pages, v_pages [n_pages, page, Hkv, d] of the type of k_new, or float8_e4m3fn (stored =
     x / scale, fp32 scales [Hkv]); kbar (optional fp32 [n_pages, Hkv, d]) receives the key
-    mean of each page written to.
+    mean of each page written to.  k_pages, v_pages and kbar do not overlap (two parts of one
+    buffer, side by side, do not; one tensor may be both caches if it gets the same rows as both).
     """
     _page_call("page_append", k_pages, stream, k_new, v_new, slot, k_pages, v_pages, k_scale, v_scale, kbar, err)
 

@@ -159,3 +159,36 @@ def test_outputs_made_for_another_stream(name):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(copies, want))
     del junk
+
+
+def test_append_refuses_keys_and_values_in_one_place():
+    x, y = (torch.randn((3, 4, 64), device=DEV).to(torch.bfloat16) for _ in range(2))
+    slot = torch.tensor([0, 1, 9], device=DEV)
+    buf = torch.zeros((6, 2, 8, 8, 64), dtype=torch.bfloat16, device=DEV)
+    one, other = buf[:, 0, :, :4], buf[:, 1, :, :4]
+    for k, v, why in ((one, one, "one tensor"), (buf[:, 0, :, :4], buf[:, 0, :, 2:6], "heads in common"),
+                      (buf[:5, 0, :, :4], buf[1:, 0, :, :4], "pages in common")):
+        with pytest.raises(ValueError, match="overlap"):
+            vkv.page_append(x, y, slot, k, v)
+        assert int(buf.count_nonzero()) == 0, why
+    flat = torch.zeros((7, 8, 4, 64), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="overlap"):
+        vkv.page_append(x, y, slot, flat[:6], flat[1:])
+    with pytest.raises(ValueError, match="overlap"):  # the same rows, stored by different scales
+        e = torch.zeros((6, 8, 4, 64), device=DEV).to(torch.float8_e4m3fn)
+        vkv.page_append(x, x, slot, e, e, k_scale=torch.ones(4, device=DEV), v_scale=torch.full((4,), 2.0, device=DEV))
+    store = torch.zeros(6 * 8 * 4 * 64 * 2, dtype=torch.float32, device=DEV)
+    k = store[:6 * 8 * 4 * 32].view(torch.bfloat16).view(6, 8, 4, 64)
+    with pytest.raises(ValueError, match="kbar overlaps"):
+        vkv.page_append(x, y, slot, k, flat[:6], kbar=store[64:64 + 6 * 4 * 64].view(6, 4, 64))
+    # side by side in one buffer, by page, by token and by head
+    slot = torch.tensor([0, 1, 3], device=DEV)
+    for k, v in ((one, other), (buf[:3, 0, :, :4], buf[3:, 0, :, :4]), (buf[:, 0, ::2, :4], buf[:, 0, 1::2, :4]),
+                 (buf[:, 0, :, :4], buf[:, 0, :, 4:])):
+        buf.zero_()
+        vkv.page_append(x, y, slot, k, v)
+        assert torch.equal(k[0, slot], x) and torch.equal(v[0, slot], y)
+        assert int(buf.count_nonzero()) == int(x.count_nonzero() + y.count_nonzero())
+    slot = torch.tensor([0, 1, 9], device=DEV)
+    vkv.page_append(x, x, slot, flat[:6], flat[:6])  # one tensor, equal rows
+    assert torch.equal(flat[1, 1], x[2])
