@@ -639,10 +639,9 @@ vkv_status vkv_page_select(const vkv_page_select_args* args, vkv_stream_t stream
  *   s_t = scale * <q, k_t>,  o = sum_t softmax(s)_t v_t,  lse = ln sum_t exp(s_t),
  * with k_t = k_scale[head] * stored for a VKV_E4M3 cache, values alike.  What the pages hold
  * beyond the visible tokens (any bits) has no effect.  A visible infinite value makes its
- * channel of o infinite or NaN.  o and lse overlap none of the inputs.  A row with no
- * visible token gives
- * o = 0 and lse = -inf; the outputs of a row with kv_len = -1 are left as they were.  A
- * length below -1 or above W * page raises VKV_DEVERR_BAD_OFFSETS and its row's outputs
+ * channel of o infinite or NaN.  o and lse overlap neither one another nor an input.
+ * A row with no visible token gives o = 0 and lse = -inf; the outputs of a row with
+ * kv_len = -1 are left as they were.  A length below -1 or above W * page raises VKV_DEVERR_BAD_OFFSETS and its row's outputs
  * are left as they were; a page number outside [0, n_pages) or a selected page outside
  * [-1, W) raises VKV_DEVERR_BAD_INDEX and its tokens do not count (selected pages past the
  * row's length do not count either).

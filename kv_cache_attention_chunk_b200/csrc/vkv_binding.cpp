@@ -337,6 +337,13 @@ PyObject* page_attn(PyObject*, PyObject* const* x, Py_ssize_t n) {
     // a row's queries may be read again after some of its outputs are written
     if (q.numel() && o.data_ptr() == q.data_ptr()) throw Refusal{"o must not be q"};
     no_overlap(o, "o");
+    {  // nor may the outputs lie in what other blocks may still read, or in one another
+      const Span os(o), ls(tensor(x[14], "lse")), qs(q), ks(tensor(x[3], "k_pages")), vs(tensor(x[4], "v_pages"));
+      if (share(os, qs)) throw Refusal{"o overlaps q"};
+      if (share(os, ks) || share(os, vs)) throw Refusal{"o overlaps the cache"};
+      if (share(ls, os) || share(ls, qs) || share(ls, ks) || share(ls, vs))
+        throw Refusal{"lse overlaps o, q or the cache"};
+    }
     vkv_page_attn_args a{};
     const int64_t R = q.size(0), H = q.size(1);
     a.R = size_of(R, "q"), a.H = size_of(H, "q");

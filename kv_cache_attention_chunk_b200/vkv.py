@@ -900,7 +900,7 @@ def page_attn(q, k_pages, v_pages, block_table, kv_len, scale=None, sink=0, wind
     left as they were).  window > 0 keeps the first `sink` and the last `window` tokens; sel
     (from page_select) the selected pages.  Returns (o [R, H, d], lse fp32 [R, H]).
     workspace: a uint8 tensor whose first PAGE_ATTN_CLEAR_BYTES were zero before its first use.
-    `out` must not overlap the inputs.
+    o and lse (given as `out`) must not overlap one another or the inputs.
     """
     R, H, d = q.shape
     if out is None:

@@ -192,3 +192,26 @@ def test_append_refuses_keys_and_values_in_one_place():
     slot = torch.tensor([0, 1, 9], device=DEV)
     vkv.page_append(x, x, slot, flat[:6], flat[:6])  # one tensor, equal rows
     assert torch.equal(flat[1, 1], x[2])
+
+
+def test_attn_refuses_outputs_that_lie_in_inputs():
+    R, H, d = 3, 4, 64
+    c = attn_case(R=R, H=H, Hkv=2, d=d, P=16, lens=[20, 5, 40], poison=False)
+    lse = torch.empty((R, H), device=DEV)
+    buf = torch.zeros((R + 1, 2 * H, d), dtype=torch.bfloat16, device=DEV)
+    for q, o in ((buf[:R, :H], buf[1:, :H]), (buf[:R, :H], buf[:R, 2:2 + H]), (buf[:R, :H], buf[:R, :H])):
+        with pytest.raises(ValueError, match="o must not be q|o overlaps q"):
+            attn_call({**c, "q": q}, out=(o, lse))
+    with pytest.raises(ValueError, match="o overlaps"):
+        attn_call(c, out=(c["k"].view(-1)[64:64 + R * H * d].view(R, H, d), lse))
+    with pytest.raises(ValueError, match="o overlaps"):
+        attn_call(c, out=(c["v"].view(-1)[:R * H * d].view(R, H, d), lse))
+    o = torch.empty((R, H, d), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="lse overlaps"):
+        attn_call(c, out=(o, o.view(-1)[:2 * R * H].view(torch.float32).view(R, H)))
+    with pytest.raises(ValueError, match="lse overlaps"):
+        attn_call(c, out=(o, c["q"].view(-1)[:2 * R * H].view(torch.float32).view(R, H)))
+    want = attn_call(c)
+    buf[:R, :H] = c["q"]  # side by side in one buffer
+    attn_call({**c, "q": buf[:R, :H]}, out=(buf[:R, H:], lse))
+    assert torch.equal(buf[:R, H:], want[0]) and torch.equal(lse, want[1])
