@@ -232,6 +232,40 @@ PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F&& body) {
   return nullptr;
 }
 
+// The arrays of a map call, in memory: what is written lies in nothing else, but that kv_len and
+// ring_pos may be updated in place.
+void map_apart(const vkv_page_map_args& a) {
+  struct Part {
+    const void* begin;
+    int64_t bytes;
+    const char* name;
+  };
+  const int64_t R = a.R, n = a.max_tokens;
+  const Part part[] = {{a.kv_len_out, 4 * R, "out['kv_len']"}, {a.ring_pos_out, 16, "out['ring']"},
+                       {a.slot, 8 * n, "out['slot']"},         {a.row, 4 * n, "out['row']"},
+                       {a.pos, 4 * n, "out['pos']"},           {a.cu, 4 * (R + 1), "out['cu']"},
+                       {a.ring, 4 * (int64_t)a.n_ring, "ring"}, {a.kv_len, 4 * R, "kv_len"},
+                       {a.new_len, 4 * R, "new_len"},          {a.ring_pos, 16, "ring_pos"}};
+  constexpr int kWritten = 7, kParts = 10;  // the first are written
+  const char* table = reinterpret_cast<const char*>(a.table);
+  const int64_t stride = 4 * a.table_stride, row = 4 * (int64_t)a.W;
+  for (int i = 0; i < kParts; ++i) {
+    const char *x = static_cast<const char*>(part[i].begin), *x_end = x + part[i].bytes;
+    if (!x) continue;
+    // the table: the first of its rows that ends behind x, if it begins before x_end
+    if (x < table + (R - 1) * stride + row && x_end > table) {
+      const int64_t off = x - table, r = off < row ? 0 : (off - row) / stride + 1;
+      if (r < R && r * stride < x_end - table) throw Refusal{std::string(part[i].name) + " and block_table overlap"};
+    }
+    for (int j = i + 1; i < kWritten && j < kParts; ++j) {
+      const char *y = static_cast<const char*>(part[j].begin), *y_end = y + part[j].bytes;
+      if (!y || x_end <= y || y_end <= x) continue;
+      if (x == y && ((i == 0 && j == 7) || (i == 1 && j == 9))) continue;
+      throw Refusal{std::string(part[i].name) + " and " + part[j].name + " overlap"};
+    }
+  }
+}
+
 // fn, stream, kv_len, new_len, table, ring, ring_pos, page, max_tokens, out_len, out_ring, slot, row, pos, cu, err
 PyObject* page_map(PyObject*, PyObject* const* x, Py_ssize_t n) {
   return guarded(n, 16, [&]() -> PyObject* {
@@ -259,6 +293,7 @@ PyObject* page_map(PyObject*, PyObject* const* x, Py_ssize_t n) {
     a.pos = vec<int32_t>(x[13], "out['pos']", at::kInt, {a.max_tokens}, dev, true);
     a.cu = vec<int32_t>(x[14], "out['cu']", at::kInt, {R + 1}, dev, true);
     a.err_word = err_word(x[15], dev);
+    if (R > 0 && a.W > 0 && a.max_tokens > 0) map_apart(a);
     return call(x[0], x[1], a);
   });
 }

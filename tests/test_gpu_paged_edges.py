@@ -215,3 +215,30 @@ def test_attn_refuses_outputs_that_lie_in_inputs():
     buf[:R, :H] = c["q"]  # side by side in one buffer
     attn_call({**c, "q": buf[:R, :H]}, out=(buf[:R, H:], lse))
     assert torch.equal(buf[:R, H:], want[0]) and torch.equal(lse, want[1])
+
+
+def test_map_refuses_arrays_that_overlap():
+    R, W, n, cap = 4, 3, 12, 8
+
+    def call(**kw):
+        big = torch.zeros(200, dtype=torch.int32, device=DEV)
+        a = {"kv_len": big[:R], "new_len": big[10:10 + R], "table": big[20:20 + R * W].view(R, W), "ring": big[40:40 + n],
+             "ring_pos": big[60:64].view(torch.int64), "out_len": big[70:70 + R], "out_ring": big[80:84].view(torch.int64),
+             "slot": big[90:90 + 2 * cap].view(torch.int64), "row": big[110:110 + cap], "pos": big[120:120 + cap],
+             "cu": big[130:131 + R]}
+        a.update({k: f(big) for k, f in kw.items()})
+        big[60:64].view(torch.int64)[1] = n
+        out = {"kv_len": a["out_len"], "ring": a["out_ring"], "slot": a["slot"], "row": a["row"], "pos": a["pos"], "cu": a["cu"]}
+        return vkv.page_map(a["kv_len"], a["new_len"], a["table"], a["ring"], a["ring_pos"], 16, cap, out=out)
+
+    call()
+    call(out_len=lambda b: b[:R], out_ring=lambda b: b[60:64].view(torch.int64))  # in place
+    wide = lambda b: b[140:140 + R * 8].view(R, 8)[:, :W]  # noqa: E731
+    call(table=wide)
+    call(table=wide, cu=lambda b: b[143:144 + R])  # between two of the table's rows
+    for kw in (dict(out_len=lambda b: b[1:1 + R]), dict(out_len=lambda b: b[9:9 + R]), dict(slot=lambda b: b[78:78 + 2 * cap].view(torch.int64)),
+               dict(pos=lambda b: b[112:112 + cap]), dict(cu=lambda b: b[2:3 + R]), dict(ring=lambda b: b[24:24 + n]),
+               dict(row=lambda b: b[44:44 + cap]), dict(out_ring=lambda b: b[62:66].view(torch.int64)),
+               dict(table=wide, cu=lambda b: b[150:151 + R]), dict(table=wide, cu=lambda b: b[144:145 + R])):
+        with pytest.raises(ValueError, match="overlap"):
+            call(**kw)
