@@ -612,7 +612,7 @@ vkv_status vkv_page_append(const vkv_page_append_args* args, vkv_stream_t stream
 typedef struct {
   int32_t R, H, Hkv, d;    /* rows; query heads (a multiple of Hkv); key heads; 64 or 128 */
   int32_t page, n_pages;
-  int32_t W;               /* table columns; R * W < 2^31, W * page < 2^31            */
+  int32_t W;               /* table columns, < 2^31 - 256; R * W < 2^31, W * page < 2^31 */
   int32_t topk;            /* 1..4096, >= sink_pages + local_pages                    */
   int32_t sink_pages, local_pages;
   int32_t q_dtype;         /* VKV_BF16 or VKV_FP16                                    */

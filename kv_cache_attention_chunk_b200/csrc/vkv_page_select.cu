@@ -389,7 +389,9 @@ extern "C" vkv_status vkv_page_select(const vkv_page_select_args* a, vkv_stream_
       a->n_pages < 1 || a->W < 1 || a->topk < 1 || a->topk > 4096 || a->sink_pages < 0 || a->local_pages < 0 ||
       (long long)a->sink_pages + a->local_pages > a->topk || a->table_stride < a->W)
     return VKV_ERR_SHAPE;
-  if ((long long)a->R * a->W > INT_MAX || (long long)a->W * a->page > INT_MAX || (long long)a->R * a->Hkv > INT_MAX)
+  // a warp of the score kernel counts columns up to 4 steps of at most 16 past the row's last
+  if ((long long)a->R * a->W > INT_MAX || (long long)a->W * a->page > INT_MAX || (long long)a->R * a->Hkv > INT_MAX ||
+      a->W > INT_MAX - 256)
     return VKV_ERR_UNSUPPORTED;
   if (!a->q.ptr || !a->kbar || !a->table || !a->kv_len || !a->sel) return VKV_ERR_NULL;
   vkv_tensor q = a->q;

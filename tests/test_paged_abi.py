@@ -135,6 +135,15 @@ def test_attn_refusals(kw, want):
     assert status("attn", **kw) == want
 
 
+def test_select_refuses_tables_whose_columns_could_overflow():
+    """The score kernel's column numbers run up to 64 past the table's width, in 32 bits."""
+    wide = dict(R=1, page=1, topk=5, workspace_bytes=1 << 62)
+    for W in (2**31 - 1, 2**31 - 64, 2**31 - 256):
+        assert status("select", W=W, table_stride=W, **wide) == 5, W
+    if not torch.cuda.is_available():  # the widest that is taken
+        assert status("select", W=2**31 - 257, table_stride=2**31, **wide) == 6
+
+
 def test_wrapper_refusals():
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     with pytest.raises(ValueError):  # not on a GPU
