@@ -583,7 +583,7 @@ vkv_status vkv_page_map(const vkv_page_map_args* args, vkv_stream_t stream);
  */
 typedef struct {
   int32_t T, Hkv, d;       /* tokens, 0..2^30; key heads, 1..4096; d in {64, 128}     */
-  int32_t page, n_pages;   /* tokens per page; pages of the cache                     */
+  int32_t page, n_pages;   /* tokens per page, 1..2^30; pages of the cache            */
   int32_t x_dtype;         /* VKV_BF16 or VKV_FP16: k_new, v_new                      */
   int32_t kv_dtype;        /* x_dtype or VKV_E4M3: the cache                          */
   int32_t reserved;        /* 0                                                       */

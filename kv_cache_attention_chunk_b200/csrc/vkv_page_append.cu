@@ -339,7 +339,8 @@ extern "C" vkv_status vkv_page_append(const vkv_page_append_args* a, vkv_stream_
   if (a->x_dtype != VKV_BF16 && a->x_dtype != VKV_FP16) return VKV_ERR_UNSUPPORTED;
   if (a->kv_dtype != a->x_dtype && a->kv_dtype != VKV_E4M3) return VKV_ERR_UNSUPPORTED;
   if (a->T < 0 || a->T > (1 << 30) || a->Hkv < 1 || a->page < 1 || a->n_pages < 1) return VKV_ERR_SHAPE;
-  if (a->Hkv > 4096) return VKV_ERR_UNSUPPORTED;
+  // the loops over a page's rows step up to 64 past the last
+  if (a->Hkv > 4096 || a->page > (1 << 30)) return VKV_ERR_UNSUPPORTED;
   if (a->kv_dtype != VKV_E4M3 && (a->k_scale || a->v_scale)) return VKV_ERR_UNSUPPORTED;
   if (!a->k.ptr || !a->v.ptr || (a->T > 0 && (!a->k_new.ptr || !a->v_new.ptr || !a->slot))) return VKV_ERR_NULL;
   if (!page_tensor_aligned(a->k, a->kv_dtype) || !page_tensor_aligned(a->v, a->kv_dtype)) return VKV_ERR_ALIGN;

@@ -135,6 +135,14 @@ def test_attn_refusals(kw, want):
     assert status("attn", **kw) == want
 
 
+def test_append_refuses_pages_whose_rows_could_overflow():
+    """The mean's loop over a page's earlier rows steps up to 64 rows past the last, in 32 bits."""
+    for page in (2**31 - 1, 2**31 - 64, 2**30 + 1):
+        assert status("append", page=page) == 5, page
+    if not torch.cuda.is_available():  # the longest that is taken
+        assert status("append", page=2**30) == 6
+
+
 def test_select_refuses_tables_whose_columns_could_overflow():
     """The score kernel's column numbers run up to 64 past the table's width, in 32 bits."""
     wide = dict(R=1, page=1, topk=5, workspace_bytes=1 << 62)
