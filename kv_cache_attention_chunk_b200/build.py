@@ -105,10 +105,22 @@ def _build_one(target: str, defines, force: bool, verbose: bool) -> str:
     return target
 
 
+def binding_tag() -> str:
+    """What the torch binding fits: this torch and this Python.  _binding.so holds the one it was built with."""
+    import torch
+    return f"vkv_binding for torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_fits() -> bool:
+    """Whether _binding.so was built for this torch and this Python."""
+    with open(BINDING, "rb") as fh:
+        return (binding_tag() + "\0").encode() in fh.read()
+
+
 def _build_binding(force: bool, verbose: bool) -> str:
     src, deps = os.path.join(CSRC, "vkv_binding.cpp"), [os.path.join(INCLUDE, "vkv.h"), os.path.abspath(__file__)]
     if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in [src, *deps]):
+            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in [src, *deps]) and binding_fits():
         return BINDING
     import torch
     home = os.path.dirname(torch.__file__)
@@ -117,7 +129,8 @@ def _build_binding(force: bool, verbose: bool) -> str:
         raise RuntimeError("g++ not found: it is required to build the torch binding")
     tmp = BINDING + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DVKV_BINDING_TAG="{binding_tag()}"',
+           "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
            "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"), src, "-o", tmp,
            "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]

@@ -423,4 +423,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
+// The torch and the Python that this file was built for: the build and the import look for it in the library.
+extern "C" __attribute__((used, visibility("default"))) const char vkv_binding_tag[] = VKV_BINDING_TAG;
+
 PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }

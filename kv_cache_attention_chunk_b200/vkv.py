@@ -26,6 +26,8 @@ from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
 import numpy as np
 import torch
 
+from . import build
+
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvkv.so")
 LIB_TEST_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvkv_test.so")
 
@@ -767,11 +769,13 @@ _binding = None
 def _page_binding():
     global _binding
     if _binding is None:
+        how = "build it with `python -m kv_cache_attention_chunk_b200.build`"
+        if os.path.exists(build.BINDING) and not build.binding_fits():  # it would load, and read another torch's tensors
+            raise RuntimeError(f"{build.BINDING} was built for another torch or Python: {how}")
         try:
             from . import _binding as b
         except ImportError as e:
-            raise RuntimeError(f"the torch binding does not load ({e}): build it with "
-                               "`python -m kv_cache_attention_chunk_b200.build`") from e
+            raise RuntimeError(f"the torch binding does not load ({e}): {how}") from e
         _binding = b
     return _binding
 

@@ -135,6 +135,25 @@ def test_attn_refusals(kw, want):
     assert status("attn", **kw) == want
 
 
+def test_binding_of_another_torch_is_rebuilt_and_never_loaded(monkeypatch):
+    assert build.binding_fits()
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not build.binding_fits()
+    commands = []
+
+    def run(cmd, **kw):
+        commands.append(cmd)
+        raise FileNotFoundError("not run")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    with pytest.raises(FileNotFoundError):  # though no file is newer than it
+        build.build()
+    assert any(str(x).endswith("vkv_binding.cpp") for x in commands[0])
+    monkeypatch.setattr(vkv, "_binding", None)
+    with pytest.raises(RuntimeError, match="another torch"):
+        vkv._page_binding()
+
+
 def test_append_refuses_pages_whose_rows_could_overflow():
     """The mean's loop over a page's earlier rows steps up to 64 rows past the last, in 32 bits."""
     for page in (2**31 - 1, 2**31 - 64, 2**30 + 1):
