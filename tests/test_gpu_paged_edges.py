@@ -242,3 +242,116 @@ def test_map_refuses_arrays_that_overlap():
                dict(table=wide, cu=lambda b: b[150:151 + R]), dict(table=wide, cu=lambda b: b[144:145 + R])):
         with pytest.raises(ValueError, match="overlap"):
             call(**kw)
+
+
+def append_dispatch(T, Hkv, P):
+    """(four warps per run, tokens per block) of an append with means, as its launch chooses them."""
+    n_sm = torch.cuda.get_device_properties(0).multi_processor_count
+    split = T * Hkv <= 8 * n_sm or P >= 64
+    return split, min(32, max(1, T * Hkv // ((16 if split else 64) * n_sm)))
+
+
+@pytest.mark.parametrize("x, kv", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("d, Hkv, P, tokens, split, slab", [
+    (64, 5, 5, 2100, False, 1), (128, 3, 16, 18000, False, 5), (128, 12, 32, 9000, False, 11), (64, 12, 16, 27000, False, 32),
+    (128, 5, 33, 64000, False, 32), (64, 3, 1, 20000, False, 6), (128, 3, 64, 13000, True, 16), (64, 12, 200, 7000, True, 32)])
+def test_append_means_of_long_prompts(x, kv, d, Hkv, P, tokens, split, slab):
+    """Prompts that start inside a page, runs that cross the blocks' slabs, several runs per slab, idle warps."""
+    gen = torch.Generator(device=DEV).manual_seed(P + d)
+    g = np.random.default_rng(P)
+    held, new = [], []
+    while sum(new) < tokens:
+        held.append(int(g.integers(0, 2 * P + 1)))
+        new.append(int(g.choice([1, g.integers(0, 2 * P + 2), g.integers(0, tokens // 5)])))
+    T = sum(new) + 2 * len(new)  # two skipped tokens behind each row's
+    got_split, got_slab = append_dispatch(T, Hkv, P)
+    assert got_split == split and abs(got_slab - slab) <= max(1, slab // 4)
+    pages = [-(-(a + b) // P) for a, b in zip(held, new)]
+    N = sum(pages) + 2
+    perm = torch.from_numpy(g.permutation(N)).to(DEV)
+    slot, upto, at = [], torch.zeros(N, dtype=torch.int64, device=DEV), 0
+    for a, b, n in zip(held, new, pages):
+        t = torch.arange(a, a + b, device=DEV)
+        own = perm[at:at + n]
+        at += n
+        slot += [own[t // P] * P + t % P, torch.full((2,), -1, device=DEV)]
+        upto.scatter_reduce_(0, own[t // P], t % P + 1, "amax")
+    slot = torch.cat(slot)
+    k, v = (torch.randn((N, P, Hkv, d), device=DEV, generator=gen).to(TYPES[kv]) for _ in range(2))
+    kn, vn = (torch.randn((T, Hkv, d), device=DEV, generator=gen).to(TYPES[x]) for _ in range(2))
+    ks = vs = None
+    if kv == "e4m3":
+        ks, vs = (torch.rand(Hkv, device=DEV, generator=gen) * 0.1 + 0.01 for _ in range(2))
+    kbar = torch.full((N, Hkv, d), 9.0, device=DEV)
+    live = slot >= 0
+    want = []
+    for cache, rows, s in ((k, kn, ks), (v, vn, vs)):
+        w = rows[live] if s is None else (rows[live].float() / s[None, :, None]).clamp(-448, 448).to(TYPES[kv])
+        w0 = cache.clone()
+        bits(w0).view(N * P, -1)[slot[live]] = bits(w).view(int(live.sum()), -1)
+        want.append(w0)
+    err = new_err()
+    vkv.page_append(kn, vn, slot, k, v, k_scale=ks, v_scale=vs, kbar=kbar, err=err)
+    assert int(err.item()) == 0
+    assert torch.equal(bits(k), bits(want[0])) and torch.equal(bits(v), bits(want[1]))
+    inside = (torch.arange(P, device=DEV)[None] < upto[:, None])[..., None, None]
+    stored = torch.where(inside, k.double(), 0.0)
+    n = upto.clamp(min=1).double()[:, None, None]
+    scale = (torch.ones(Hkv, device=DEV) if ks is None else ks).double()[None, :, None]
+    # n fp32 additions, a division, a product: at most (n + 2) half-ulps of the sum of magnitudes
+    tol = (n + 2) * 2.0**-24 * stored.abs().sum(1) / n * scale
+    off = (kbar.double() - stored.sum(1) / n * scale).abs()
+    written = upto > 0
+    assert (off[written] <= tol[written]).all() and (kbar[~written] == 9.0).all()
+
+
+@pytest.mark.parametrize("R, H, Hkv, W, steps", [(3, 4, 2, 2900, 1), (6, 10, 5, 6000, 10), (5, 9, 9, 9001, 16), (64, 24, 12, 700, 16)])
+def test_select_several_steps_per_warp(R, H, Hkv, W, steps):
+    """d = 128, by the number of steps that a warp of the score kernel takes; rows that end inside a step."""
+    n_sm = torch.cuda.get_device_properties(0).multi_processor_count
+    assert min(16, -(-R * Hkv * -(-W // 8) // (16 * n_sm))) == steps
+    P, d = 2, 128
+    gen = torch.Generator(device=DEV).manual_seed(W)
+    lens = [W * P - i % 16 * 37 for i in range(R)]
+    lens[1] = 40 * P - 1
+    kbar = torch.randn((300, Hkv, d), device=DEV, generator=gen)
+    table = torch.randint(0, 300, (R, W), dtype=torch.int32, device=DEV, generator=gen)
+    q = torch.randn((R, H, d), device=DEV, generator=gen).to(torch.bfloat16)
+    for topk, first, last in ((33, 2, 3),):
+        err = new_err()
+        sel = vkv.page_select(q, kbar, table, i32(lens), P, topk, first, last, err=err)
+        few = [0, 1, 2, R - 1] if R > 16 else list(range(R))
+        want = oracle.page_select(f64(q[few]), f64(kbar), table[few].cpu().numpy(), [lens[r] for r in few], P, topk, first, last)
+        assert int(err.item()) == 0 and np.array_equal(sel[few].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("q, kv", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("H, Hkv, d, lens", [(6, 2, 128, [400, 77]), (8, 8, 64, [5000, 2003, 33]), (12, 1, 128, [9001]), (3, 1, 64, [30011, 1])])
+def test_attn_scores_far_apart(q, kv, H, Hkv, d, lens):
+    """Softmaxes that one or few tokens win, maxima that move often and lie far apart where parts are joined.
+
+    q, k and the scales are small whole numbers (times powers of two), so a score s is exact.  Its
+    log2 form x, |x| <= X, carries at most 3 x 2^-24 X from c's rounding, the product and the maximum's
+    subtraction, so a weight is off by e = 3 x 2^-24 X + 2^-21 (the exponential).  A move of the maximum
+    multiplies what came before by one more such factor, but shrinks it 2^4 times at least, and a part's
+    weight in the joins is one more: 4 e in all.  The sum over n tokens adds n 2^-24, a weight's two
+    16-bit parts leave 2^-16.
+    """
+    c = attn_case(R=len(lens), H=H, Hkv=Hkv, d=d, P=16, lens=lens, q=q, kv=kv)
+    gen = torch.Generator(device=DEV).manual_seed(H)
+    whole = lambda t: torch.randint(-3, 4, t.shape, device=DEV, generator=gen).to(t.dtype)  # noqa: E731
+    holes = c["k"].float().isnan()
+    c["q"] = whole(c["q"])
+    c["k"] = torch.where(holes, float("nan"), whole(c["k"]).float()).to(c["k"].dtype)
+    c["scale"] = 0.5
+    if c["ks"] is not None:
+        c["ks"] = torch.tensor([2.0 ** (i % 3 - 1) for i in range(Hkv)], device=DEV)
+    o, lse = attn_call(c)
+    ro, rl, terms = attn_ref(c)
+    X, vmax, n = 1.45 * terms[..., 0] + 16, terms[..., 1], terms[..., 2]
+    e_w = 4 * (3 * 2.0**-24 * X + 2.0**-21) + n * 2.0**-24
+    info = torch.finfo(TYPES[q])
+    tol = (2 * e_w + 2.0**-15)[..., None] * vmax[..., None] + info.eps / 2 * np.abs(ro) * 1.01
+    assert (tol < 0.02 * vmax[..., None]).all()  # a wrong row of values does not pass
+    assert (np.abs(f64(o) - ro) <= tol).all()
+    assert (np.abs(f64(lse) - rl) <= e_w + 2.0**-22 * np.abs(rl) + 2.0**-22).all()
