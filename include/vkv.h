@@ -571,9 +571,9 @@ vkv_status vkv_page_map(const vkv_page_map_args* args, vkv_stream_t stream);
  * stored = x, or for a VKV_E4M3 cache e4m3(x / scale[head]) (fp32 quotient, round to
  * nearest even, magnitudes above 448 become 448, NaN stays NaN).  Tokens with slot < 0 are
  * skipped; a slot >= n_pages * page raises VKV_DEVERR_BAD_INDEX and is skipped.  Slots of
- * one call are distinct (else it is open which token's row is kept).  k and v do not overlap,
- * unless they are one array that gets the same rows as both; kbar overlaps neither.  k_new and
- * v_new may lie in the cache, though not in rows that the call writes.
+ * one call are distinct (else it is open what their rows and means hold).  k and v do not
+ * overlap, unless they are one array that gets the same rows as both; kbar overlaps neither.
+ * k_new and v_new may lie in the cache, though not in rows that the call writes.
  * kbar (optional): receives, for each page written to, the mean of its stored keys
  * (times k_scale) from the page's first token to the call's last one there, as fp32 -- the
  * page's representative for vkv_page_select.  The call's tokens of one page then have to

@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
 // lanes each, one row per group and load, kRun loads in flight) first add the page's earlier
 // rows, read from the cache, then copy the run's rows and add what they store; the groups'
 // sums meet by shuffles, in a fixed order.  SPLIT: the block's four warps share each run of one
-// head instead, and meet in shared memory: for calls of few runs (64 rows' next tokens: 3.6
-// us against 6.7 us) and pages of many tokens.
+// head instead, and meet in shared memory: for calls of few runs (64 rows' next tokens: 4.1
+// us against 5.5 us) and pages of many tokens.
 constexpr int kMeanWarps = 4;
 constexpr int kRun = 4;
 
@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(kMeanWarps * 32, 5) append_mean_kernel(const A
 template <int D, typename IN, bool E4M3>
 cudaError_t launch(AppendParams& p, int n_sm, cudaStream_t st) {
   if (p.kbar) {
-    // four warps per run where runs are few or long (pages of 64 tokens: 29.9 against 31.8 us for
-    // 17000 tokens; of 16 tokens 32 against 24 us, for half of the lanes have no row); tokens per
+    // four warps per run where runs are few or long (pages of 64 tokens: 29.2 against 31.0 us for
+    // 17000 tokens; of 16 tokens, e4m3, 27.9 against 19.2 us, for half of the lanes have no row); tokens per
     // block so that about `warps` warps per SM have one
     const bool split = (long long)p.T * p.Hkv <= 8ll * n_sm || p.page >= 64;
     const long long warps = split ? 16 : 64;

@@ -49,7 +49,7 @@ constexpr float kSlack = 4.f;  // log2: how far a score may exceed the running m
 constexpr int kMinTiles = 2;
 constexpr float kShareRoot = 0.045f;
 // Calls of at most this many tiles per warp give each unit whole blocks (two rows of 520 tokens,
-// 8 key heads of 64 channels: 9.8 us, on the line 16.3; one row of 1560 tokens 12.0 and 14.1; above
+// 8 key heads of 64 channels: 8.8 us, on the line 16.7; one row of 1560 tokens 11.0 and 12.7; above
 // it equal shares count for more)
 constexpr int kWholeMost = 8;
 
@@ -911,8 +911,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, F8, NT>::BLOCKS) page_attn_
       float top[HW], sum[HW];
       V4 x[HW];
       // part 0 lies among its block's lasts, the others among their blocks' firsts
-      // loads in flight per head; fewer where a warp has four heads (37 rows of 2310 tokens, 12 heads
-      // per key head: 63.3 us with 8, 59.9 with 4; one row of 131072 tokens 49.6 and 51.7)
+      // loads in flight per head; fewer where a warp has four heads (37 rows of 2310 tokens, e4m3, 12
+      // heads per key head: 63.3 us with 8, 59.9 with 4; one row of 131072 tokens 49.6 and 51.7)
       constexpr int kBatch = NT == 1 ? 8 : 4;
       const int b0 = first >> jp, stride = (2 * hcw) << jp;
       const size_t row1 = (size_t)(b0 + 1) * stride + (first & jp) * hcw, row0 = row1 - (hcw << jp);

@@ -5,7 +5,8 @@
 // result, and the tokens, the new table entries and the returned pages can be spread over
 // the grid's threads, each of which finds its row by bisection of the scan in shared memory.
 // Where lengths or ring positions are updated in place, they may be written only after every
-// block has read them: those steps run as one cluster, with a cluster barrier in between.
+// block has read them: those steps run as one cluster of up to 8 blocks, with a cluster barrier in
+// between (256 rows that decode 5.9 us, apart 5.5; 48 rows' prompts of up to 4680 tokens 18, apart 4.3).
 //
 // Bound: latency.  A decoding step moves some tens of KB; its time is the launch, two
 // dependent reads (lengths, then ring or table) and the stores.  A thread takes kTok tokens

@@ -903,7 +903,10 @@ def page_attn(q, k_pages, v_pages, block_table, kv_len, scale=None, sink=0, wind
     float8_e4m3fn with fp32 scales [Hkv]; kv_len int32 [R] (-1: no request, its outputs are
     left as they were).  window > 0 keeps the first `sink` and the last `window` tokens; sel
     (from page_select) the selected pages.  Returns (o [R, H, d], lse fp32 [R, H]).
-    workspace: a uint8 tensor whose first PAGE_ATTN_CLEAR_BYTES were zero before its first use.
+    workspace: a uint8 tensor of vkv_page_attn_workspace_size bytes whose first PAGE_ATTN_CLEAR_BYTES
+    were zero before its first use.  Without one, calls that are being captured into a graph get one
+    each and clear it in every replay (a kernel more per call): a captured step passes its own, the same
+    to all its calls, and another one to each graph that may run beside it.
     o and lse (given as `out`) must not overlap one another or the inputs.
     """
     R, H, d = q.shape
