@@ -329,9 +329,9 @@ def block_order(sel_idx, out=None, stream=None):
     """Query-block order [B*H, nQblk] grouping similar selections, from a selection
     sel_idx (device int32 [B*H, nQblk, topk], e.g. the sel_out of chunk_attn_block_sparse
     with kbar), for a later call's qblk_order."""
-    sel_idx = sel_idx.contiguous()
+    sel_idx = _contiguous(sel_idx, stream)
     BH, n_qblk, topk = sel_idx.shape
-    order = out if out is not None else torch.empty((BH, n_qblk), dtype=torch.int32, device=sel_idx.device)
+    order = out if out is not None else _new_outputs(sel_idx, stream, ((BH, n_qblk), torch.int32))[0]
     _check(vkv_block_order(sel_idx.data_ptr(), order.data_ptr(), BH, n_qblk, topk, _stream(stream)),
            "vkv_block_order")
     return order
@@ -412,6 +412,43 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _handle(di, stream):
+    """The stream handle for a call on device `di` (-1, no GPU tensor: refused by the call)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(di) if di >= 0 else 0
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _stream_of(di, sh):
+    """The torch stream of a handle on device `di`."""
+    return torch.cuda.ExternalStream(sh, device=di) if sh else torch.cuda.default_stream(di)
+
+
+def _made_on(x, stream, make):
+    """make()'s tensors, on the device of `x`, for a call on `stream`: memory of that stream (what the current
+    stream last used could still be written there), and not handed out again, once they are freed, before
+    the current stream is done with what it has of them by then.  The caller orders the inputs before
+    `stream`, and `stream` before what uses the results."""
+    di = x.get_device()
+    if stream is None or di < 0 or _handle(di, stream) == torch._C._cuda_getCurrentRawStream(di):
+        return make()
+    with torch.cuda.stream(_stream_of(di, _handle(di, stream))):
+        out = make()
+    for y in out:
+        y.record_stream(torch.cuda.current_stream(di))
+    return out
+
+
+def _new_outputs(x, stream, *specs):
+    """Tensors (shape, type) on the device of `x` for a call on `stream` to write."""
+    return _made_on(x, stream, lambda: [torch.empty(shape, dtype=t, device=x.device) for shape, t in specs])
+
+
+def _contiguous(x, stream):
+    """`x`, or a copy that a call on `stream` may read, made there."""
+    return x if x.is_contiguous() else _made_on(x, stream, lambda: [x.contiguous()])[0]
+
+
 def tensor_desc(x: torch.Tensor) -> vkv_tensor:
     """[B, L, H, d] bf16 with a contiguous last axis -> vkv_tensor."""
     if x.dim() != 4 or x.dtype != torch.bfloat16 or x.stride(3) != 1:
@@ -450,7 +487,7 @@ def _base_args(mode, q, Lkv, d, scale, k_desc, v_desc, err):
 _attn_ws: dict = {}  # (device index, stream handle) -> uint8 device buffer, grown on demand
 
 
-def _attn_workspace(a: vkv_attn_args, q: torch.Tensor, stream_handle: int, split: bool, workspace):
+def _attn_workspace(a: vkv_attn_args, q: torch.Tensor, stream, split: bool, workspace):
     """Point the call at a key-axis split workspace: the caller's, or one kept per
     (device, stream) by this module; none when split is False or the schedule
     splits nothing.  Returns the buffer (kept alive by the caller until launch)."""
@@ -463,20 +500,19 @@ def _attn_workspace(a: vkv_attn_args, q: torch.Tensor, stream_handle: int, split
     need = vkv_chunk_attn_workspace_size(a)
     if need == 0:
         return None
-    key = (q.device.index, stream_handle)
+    key = (q.device.index, _stream(stream))
     buf = _attn_ws.get(key)
     if buf is None or buf.numel() < need:
-        buf = torch.empty(need, dtype=torch.uint8, device=q.device)
+        buf, = _new_outputs(q, stream, (need, torch.uint8))
         _attn_ws[key] = buf
     a.workspace = buf.data_ptr()
     a.workspace_bytes = buf.numel()
     return buf
 
 
-def _new_out(q):
+def _new_out(q, stream):
     B, Lq, H, d = q.shape
-    return (torch.empty((B, Lq, H, d), dtype=torch.bfloat16, device=q.device),
-            torch.empty((B, H, Lq), dtype=torch.float32, device=q.device))
+    return tuple(_new_outputs(q, stream, ((B, Lq, H, d), torch.bfloat16), ((B, H, Lq), torch.float32)))
 
 
 def segments_args(q, k, v, branches, scale=None, err=None) -> vkv_attn_args:
@@ -510,10 +546,10 @@ def chunk_attn_segments(q, k, v, branches, scale=None, merged=True, err=None, st
     if out is None:
         res["o"], res["lse"] = [], []
         for _ in range(nb):
-            o, l = _new_out(q)
+            o, l = _new_out(q, stream)
             res["o"].append(o)
             res["lse"].append(l)
-        res["o_merged"], res["lse_merged"] = _new_out(q) if (merged and nb == 2) else (None, None)
+        res["o_merged"], res["lse_merged"] = _new_out(q, stream) if (merged and nb == 2) else (None, None)
     for i in range(nb):
         a.o[i] = tensor_desc(res["o"][i])
         a.lse[i] = res["lse"][i].data_ptr()
@@ -521,7 +557,7 @@ def chunk_attn_segments(q, k, v, branches, scale=None, merged=True, err=None, st
         a.o_merged = tensor_desc(res["o_merged"])
         a.lse_merged = res["lse_merged"].data_ptr()
     sh = _stream(stream)
-    ws = _attn_workspace(a, q, sh, split, workspace)  # noqa: F841 (alive until the launch)
+    ws = _attn_workspace(a, q, stream, split, workspace)  # noqa: F841 (alive until the launch)
     _check(vkv_chunk_attn(a, sh), "vkv_chunk_attn")
     return res
 
@@ -541,7 +577,7 @@ def chunk_attn_block_sparse(q, k, v, persist_idx, sel_idx, window_blk0, n_win_bl
     """
     d = q.shape[3]
     a = _base_args(MODE_BLOCK_SPARSE, q, k.shape[1], d, scale, tensor_desc(k), tensor_desc(v), err)
-    persist_idx = persist_idx.contiguous()
+    persist_idx = _contiguous(persist_idx, stream)
     a.persist_idx = persist_idx.data_ptr() if persist_idx.numel() else None
     a.n_persist = persist_idx.shape[-1]
     if kbar is not None:
@@ -556,19 +592,19 @@ def chunk_attn_block_sparse(q, k, v, persist_idx, sel_idx, window_blk0, n_win_bl
             a.sel_out = sel_out.data_ptr()
         a.topk = int(topk)
     else:
-        sel_idx = sel_idx.contiguous()
+        sel_idx = _contiguous(sel_idx, stream)
         a.sel_idx = sel_idx.data_ptr() if sel_idx.numel() else None
         a.topk = sel_idx.shape[-1]
     a.window_blk0 = int(window_blk0)
     a.n_win_blk = int(n_win_blk)
     if qblk_order is not None:
-        qblk_order = qblk_order.contiguous()
+        qblk_order = _contiguous(qblk_order, stream)
         a.qblk_order = qblk_order.data_ptr()
-    o, l = out if out is not None else _new_out(q)
+    o, l = out if out is not None else _new_out(q, stream)
     a.o[0] = tensor_desc(o)
     a.lse[0] = l.data_ptr()
     sh = _stream(stream)
-    ws = _attn_workspace(a, q, sh, split, workspace)  # noqa: F841 (alive until the launch)
+    ws = _attn_workspace(a, q, stream, split, workspace)  # noqa: F841 (alive until the launch)
     _check(vkv_chunk_attn(a, sh), "vkv_chunk_attn")
     return o, l
 
@@ -587,11 +623,11 @@ def chunk_attn_ragged(q, k_flat, v_flat, cu_seqlens, cu_seqlens_host=None, scale
     if cu_seqlens_host is not None:
         host = np.ascontiguousarray(np.asarray(cu_seqlens_host, dtype=np.int32))
         a.cu_seqlens_host = host.ctypes.data_as(POINTER(c_int32))
-    o, l = out if out is not None else _new_out(q)
+    o, l = out if out is not None else _new_out(q, stream)
     a.o[0] = tensor_desc(o)
     a.lse[0] = l.data_ptr()
     sh = _stream(stream)
-    ws = _attn_workspace(a, q, sh, split, workspace)  # noqa: F841 (alive until the launch)
+    ws = _attn_workspace(a, q, stream, split, workspace)  # noqa: F841 (alive until the launch)
     _check(vkv_chunk_attn(a, sh), "vkv_chunk_attn")
     return o, l
 
@@ -613,24 +649,23 @@ def block_select(q, k, window_blk0, n_win_blk, topk, workspace=None, scores=Fals
     a.window_blk0, a.n_win_blk, a.topk = int(window_blk0), int(n_win_blk), int(topk)
     a.q = tensor_desc(q)
     a.k = tensor_desc(k)
-    idx = out_idx if out_idx is not None else torch.empty((B * H, n_qblk, topk), dtype=torch.int32,
-                                                          device=q.device)
+    idx = out_idx if out_idx is not None else _new_outputs(q, stream, ((B * H, n_qblk, topk), torch.int32))[0]
     a.out_idx = idx.data_ptr()
     sc = None
     if scores:
-        sc = torch.empty((B * H, n_qblk, n_win_blk), dtype=torch.float32, device=q.device)
+        sc, = _new_outputs(q, stream, ((B * H, n_qblk, n_win_blk), torch.float32))
         a.out_scores = sc.data_ptr()
     need = vkv_block_select_workspace_size(B, H, Lq, n_win_blk, 64, d)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace, = _new_outputs(q, stream, (need, torch.uint8))
     a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel() * workspace.element_size()
     a.err_word = err.data_ptr() if err is not None else None
     if kbar is not None:
-        kbar = kbar.contiguous()
+        kbar = _contiguous(kbar, stream)
         a.kbar = kbar.data_ptr()
     if order and out_order is None:
-        out_order = torch.empty((B * H, n_qblk), dtype=torch.int32, device=q.device)
+        out_order, = _new_outputs(q, stream, ((B * H, n_qblk), torch.int32))
     if out_order is not None:
         a.out_order = out_order.data_ptr()
     _check(vkv_block_select(a, _stream(stream)), "vkv_block_select")
@@ -642,7 +677,7 @@ def block_select(q, k, window_blk0, n_win_blk, topk, workspace=None, scores=Fals
 def block_pool(x, blk0, n_blk, stream=None, out=None):
     """fp32 mean of each 64-row block [blk0, blk0 + n_blk) of x [B, L, H, d] -> [B*H, n_blk, d]."""
     B, L, H, d = x.shape
-    o = out if out is not None else torch.empty((B * H, n_blk, d), dtype=torch.float32, device=x.device)
+    o = out if out is not None else _new_outputs(x, stream, ((B * H, n_blk, d), torch.float32))[0]
     _check(vkv_block_pool(tensor_desc(x), B, L, H, d, int(blk0), int(n_blk), o.data_ptr(), _stream(stream)),
            "vkv_block_pool")
     return o
@@ -650,7 +685,7 @@ def block_pool(x, blk0, n_blk, stream=None, out=None):
 
 def lse_merge(o_a, lse_a, o_b, lse_b, stream=None, out=None):
     B, Lq, H, d = o_a.shape
-    o, l = out if out is not None else _new_out(o_a)
+    o, l = out if out is not None else _new_out(o_a, stream)
     _check(vkv_lse_merge(tensor_desc(o_a), lse_a.data_ptr(), tensor_desc(o_b), lse_b.data_ptr(),
                          tensor_desc(o), l.data_ptr(), B, H, Lq, d, _stream(stream)), "vkv_lse_merge")
     return o, l
@@ -675,9 +710,7 @@ def compact_cache(k, v, rules, frame_tokens, hist_frames, cur_frames, recent_fra
     rows = vkv_compact_rows(a)
     if rows < 0:
         raise VkvError(-rows, "vkv_compact_rows")
-    k_out = torch.empty((rows, d), dtype=k.dtype, device=k.device)
-    v_out = torch.empty((rows, d), dtype=v.dtype, device=v.device)
-    cu_dev = torch.empty(B * H + 1, dtype=torch.int32, device=k.device)
+    k_out, v_out, cu_dev = _new_outputs(k, stream, ((rows, d), k.dtype), ((rows, d), v.dtype), (B * H + 1, torch.int32))
     cu_host = np.zeros(B * H + 1, dtype=np.int32)
     a.k_out, a.v_out, a.out_rows = k_out.data_ptr(), v_out.data_ptr(), rows
     a.cu_seqlens = cu_dev.data_ptr()
@@ -694,22 +727,22 @@ def persist_update(q, k, persist_idx, evict_blk0, n_evict, scores=False, err=Non
     Returns (new persistent ids [B*H, C] ascending, candidate scores [B*H, C + n_evict] or None).
     """
     B, Lq, H, d = q.shape
-    persist_idx = persist_idx.contiguous()
+    persist_idx = _contiguous(persist_idx, stream)
     C = persist_idx.shape[-1]
     a = vkv_persist_args()
     a.B, a.H, a.d, a.block, a.Lq, a.Lkv = B, H, d, 64, Lq, k.shape[1]
     a.q, a.k = tensor_desc(q), tensor_desc(k)
     a.persist_idx, a.n_persist = persist_idx.data_ptr(), C
     a.evict_blk0, a.n_evict = int(evict_blk0), int(n_evict)
-    idx = out_idx if out_idx is not None else torch.empty((B * H, C), dtype=torch.int32, device=q.device)
+    idx = out_idx if out_idx is not None else _new_outputs(q, stream, ((B * H, C), torch.int32))[0]
     a.out_idx = idx.data_ptr()
     sc = None
     if scores:
-        sc = torch.empty((B * H, C + int(n_evict)), dtype=torch.float32, device=q.device)
+        sc, = _new_outputs(q, stream, ((B * H, C + int(n_evict)), torch.float32))
         a.out_scores = sc.data_ptr()
     need = vkv_persist_update_workspace_size(B, H, Lq, C, int(n_evict), 64, d)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace, = _new_outputs(q, stream, (need, torch.uint8))
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
     a.err_word = err.data_ptr() if err is not None else None
     _check(vkv_persist_update(a, _stream(stream)), "vkv_persist_update")
@@ -741,8 +774,8 @@ def latent_attn(q, kv, d_c, scale=None, kr=None, err=None, stream=None, out=None
         if kr is not None:
             a.kr = latent_desc(kr)
     if out is None:
-        o = torch.empty((B, Lq, H, d_c), dtype=torch.bfloat16, device=q.device)
-        l = torch.empty((B, H, Lq), dtype=torch.float32, device=q.device) if lse else None
+        o, = _new_outputs(q, stream, ((B, Lq, H, d_c), torch.bfloat16))
+        l = _new_outputs(q, stream, ((B, H, Lq), torch.float32))[0] if lse else None
     else:
         o, l = out
     a.o = tensor_desc(o)
@@ -757,7 +790,6 @@ def latent_attn(q, kv, d_c, scale=None, kr=None, err=None, stream=None, out=None
 # ---------------------------------------------------------------------------
 # These calls run once per layer and token; their arguments are checked and marshalled by
 # csrc/vkv_binding.cpp (a refused one is a ValueError), which calls the same entry points.
-# With `stream`, the caller orders the inputs before that stream and that stream before what uses the results.
 _page_attn_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, cleared once (the call leaves it clear)
 _NO_WORKSPACE = torch.empty(0, dtype=torch.uint8)
 _page_select_ws: dict = {}  # (device index, stream handle) -> uint8 buffer, grown on demand
@@ -793,32 +825,6 @@ def _page_call(name, x, stream, *args):
             status = fn(address, sh, *args)
     if status:
         _check(status, "vkv_" + name)
-
-
-def _handle(di, stream):
-    """The stream handle for a call on device `di` (-1, no GPU tensor: refused by the call)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(di) if di >= 0 else 0
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _stream_of(di, sh):
-    """The torch stream of a handle on device `di`."""
-    return torch.cuda.ExternalStream(sh, device=di) if sh else torch.cuda.default_stream(di)
-
-
-def _new_outputs(x, stream, *specs):
-    """Tensors (shape, type) on the device of `x` for a call on `stream` to write: memory of that stream
-    (what the current stream last used could still be written there), and not handed out again, once they
-    are freed, before the current stream is done with what it has of them by then."""
-    di = x.get_device()
-    if stream is None or di < 0 or _handle(di, stream) == torch._C._cuda_getCurrentRawStream(di):
-        return [torch.empty(shape, dtype=t, device=x.device) for shape, t in specs]
-    with torch.cuda.stream(_stream_of(di, _handle(di, stream))):
-        out = [torch.empty(shape, dtype=t, device=x.device) for shape, t in specs]
-    for y in out:
-        y.record_stream(torch.cuda.current_stream(di))
-    return out
 
 
 def page_map(kv_len, new_len, block_table, ring, ring_pos, page_size, max_tokens, out=None, err=None, stream=None):
