@@ -888,7 +888,9 @@ def page_select(q, kbar, block_table, kv_len, page_size, topk, sink_pages=0, loc
     """The `topk` pages that each row and key head attends to (vkv_page_select).
 
     q [R, H, d]; kbar fp32 [n_pages, Hkv, d], the pages' key means (page_append keeps them).
-    Returns int32 [R, Hkv, topk]: logical page numbers ascending, then -1.
+    Returns int32 [R, Hkv, topk]: logical page numbers ascending, then -1 (`out` lies in none of the inputs).
+    workspace: a uint8 tensor of vkv_page_select_workspace_size bytes (8 per row, key head and table
+    column); without one, this module keeps the largest that a stream has needed, as long as it is loaded.
     """
     R, Hkv = q.shape[0], kbar.shape[1]
     sel = out if out is not None else _new_outputs(q, stream, ((R, Hkv, topk), torch.int32))[0]
